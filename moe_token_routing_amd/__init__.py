@@ -1,7 +1,8 @@
 """MoE routing-and-combine hot path on MI355X (gfx950).
 
 A thin Python binding over the C ABI of libmoe_routing.so (declared in
-include/moe_routing.h). Every step runs in the library's HIP kernels; this
+include/moe_routing.h, and in include/moe_training.h for the router's training
+operators, whose functions are in training.py). Every step runs in the library's HIP kernels; this
 module only checks tensors, allocates outputs when the caller did not pass
 them, and forwards raw device pointers and the current HIP stream. PyTorch
 supplies device memory and streams.
@@ -56,6 +57,26 @@ _SIGNATURES = {
                                              _c_int, _c_int, _c_int, _vp, _vp, _vp, _c_size, _vp]),
 }
 
+# include/moe_training.h
+_TRAINING_SIGNATURES = {
+    "moe_balance_loss_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "moe_balance_loss": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int, _vp, _vp, _vp, _vp,
+                                  _vp, _c_size, _vp]),
+    "moe_balance_loss_backward": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_int, _c_int, _c_int, _c_int,
+                                           _c_int, _vp, _vp]),
+    "moe_distill_loss_workspace_bytes": (_c_size, [_c_int, _c_int]),
+    "moe_distill_loss": (_c_int, [_vp, _vp, _vp, _vp, _c_int, _c_float, _c_int, _c_int, _c_int, _vp, _vp, _vp,
+                                  _vp, _c_size, _vp]),
+    "moe_distill_loss_backward": (_c_int, [_vp, _vp, _vp, _vp, _vp, _vp, _c_int, _c_float, _c_int, _c_int, _c_int,
+                                           _c_int, _vp, _vp]),
+    "moe_route_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int, _c_int, _c_int]),
+    "moe_route_backward": (_c_int, [_vp, _vp, _vp, _c_int, _vp, _vp, _vp, _vp, _vp, _c_float, _c_int, _c_int, _c_int,
+                                    _c_int, _vp, _vp, _vp, _vp, _c_size, _vp]),
+    "moe_combine_backward_workspace_bytes": (_c_size, [_c_int, _c_int, _c_int]),
+    "moe_combine_backward": (_c_int, [_vp, _vp, _c_int, _vp, _vp, _vp, _c_float, _c_float, _c_int, _c_int, _c_int,
+                                      _vp, _vp, _vp, _vp, _c_size, _vp]),
+}
+
 
 class MoeError(RuntimeError):
     """A call returned a nonzero status."""
@@ -72,7 +93,7 @@ def lib() -> ctypes.CDLL:
         if not os.path.exists(LIB_PATH):
             raise RuntimeError("libmoe_routing.so is not built; run `python -m moe_token_routing_amd.build`")
         handle = ctypes.CDLL(LIB_PATH)
-        for name, (res, args) in _SIGNATURES.items():
+        for name, (res, args) in {**_SIGNATURES, **_TRAINING_SIGNATURES}.items():
             fn = getattr(handle, name)
             fn.restype = res
             fn.argtypes = args
@@ -441,3 +462,9 @@ def _expert_fc1(fn, rows_per_col, x_packed, x_scales, x_gs, perm, offsets, k, w_
         _ptr(w_packed), _ptr(w_scales), _ptr(w_gs), _ptr(y_gs), K, N, E,
         _ptr(y_packed), _ptr(y_scales), _ptr(workspace), workspace.numel(), _stream(dev)))
     return y_packed, y_scales
+
+
+from .training import (MOE_SCORE_SIGMOID, MOE_SCORE_SOFTMAX, balance_loss, balance_loss_backward,  # noqa: E402
+                       balance_loss_workspace_bytes, combine_backward, combine_backward_workspace_bytes,
+                       distill_loss, distill_loss_backward, distill_loss_workspace_bytes, route_backward,
+                       route_backward_workspace_bytes)
