@@ -50,6 +50,13 @@ __device__ __forceinline__ void split_pair(float x0, float x1, uint32_t& p0, uin
 
 constexpr int kPrepRows = 32, kPrepCols = 128, kPrepBlock = 256;
 constexpr int kPrepStride = kPrepCols + 4;
+constexpr int kPrepLoads = kPrepRows * kPrepCols / 4 / kPrepBlock;   // 16-byte pieces of the tile per thread
+constexpr int kSplitQuads = 4;                                       // 16-byte pieces of a row split per thread
+
+// Four floats at any 4-byte aligned address (rows of an E that is not a
+// multiple of four): still one 16-byte access.
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x4_any __attribute__((ext_vector_type(4), aligned(4)));
 
 // Eight values -> np planes of a fragment lane, plane p 64 lanes further on.
 __device__ __forceinline__ void write_fragment(const float (&v)[8], int np, u32x4* __restrict__ out) {
@@ -67,135 +74,203 @@ __device__ __forceinline__ void write_fragment(const float (&v)[8], int np, u32x
         if (p < np) out[p * kWave] = q[p];
 }
 
-// Block (x, y): tokens [32 x, +32), experts [128 y, +128). Fragments of a
-// matrix with rows m and summation index c: [m / 32][c / 16][plane][lane], lane
-// l holding row l % 32, c = 8 (l / 32) .. +8.
-//   frag_h: rows tokens, summed over experts (np_h planes)
-//   frag_w: rows experts, summed over tokens (three planes)
-// row_bits: for every 16 tokens a word, one bit each, set for valid ones.
-// d_aux may be d_logits: a block reads its tile before it writes it.
-__global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(
-    const float* __restrict__ d_topk_w, const float* d_aux, const float* __restrict__ logits,
-    const int32_t* __restrict__ ids, const float* __restrict__ topk_w, const uint8_t* __restrict__ mask, int T,
-    int E, int k, float* d_logits, u32x4* __restrict__ frag_h, int np_h, u32x4* __restrict__ frag_w,
-    uint32_t* __restrict__ row_bits, uint32_t* __restrict__ zeros) {
-    __shared__ float tile[kPrepRows * kPrepStride];
-    __shared__ int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
-    __shared__ float pick_v[kPrepRows][MOE_MAX_TOPK];
-    const int tid = threadIdx.x;
-    const int t0 = blockIdx.x * kPrepRows, e0 = blockIdx.y * kPrepCols;
-    if (zeros && blockIdx.x == 0 && blockIdx.y == 0)
-        for (int i = tid; i < static_cast<int>(kZeroBytes / 4); i += kPrepBlock) zeros[i] = 0;
+// FP32 rows to split into BF16 planes [np][rows][H].
+struct SplitArgs {
+    const float* x;        // NULL: nothing to split
+    const uint8_t* mask;   // rows whose byte is zero become zeros; NULL: none
+    int rows, np;
+    uint16_t* planes;
+};
 
-    for (int i = tid; i < kPrepRows * kPrepCols; i += kPrepBlock) {
-        const int r = i / kPrepCols, c = i - r * kPrepCols;
-        const int t = t0 + r, e = e0 + c;
-        float v = 0.f;
-        if (d_aux && t < T && e < E && mask[t]) v = d_aux[static_cast<size_t>(t) * E + e];
-        tile[r * kPrepStride + c] = v;
-    }
-    if (d_topk_w) {
-        // eight threads a token
-        const int r = tid >> 3, sub = tid & 7;
-        const int t = t0 + r;
-        const bool ok = t < T && mask[t] != 0;
-        float s = 0.f;
-        for (int j = sub; j < k; j += 8) {
-            const size_t at = static_cast<size_t>(t) * k + j;
-            int id = -1;
-            if (ok) {
-                id = ids[at];
-                if (id < 0 || id >= E) id = -1;
-            }
-            pick_id[r][j] = id;
-            if (id >= 0) s = __builtin_fmaf(topk_w[at], d_topk_w[at], s);
-        }
-        s = group_sum(s, 8);
-        for (int j = sub; j < k; j += 8) {
-            const int id = pick_id[r][j];
-            float v = 0.f;
-            if (id >= e0 && id < e0 + kPrepCols) {
-                const size_t at = static_cast<size_t>(t) * k + j;
-                // 1 - sigmoid(l) = 1 / (1 + exp(l))
-                v = topk_w[at] * (d_topk_w[at] - s) / (1.f + expf(logits[static_cast<size_t>(t) * E + id]));
-            }
-            pick_v[r][j] = v;
-        }
-        __syncthreads();
-        for (int j = sub; j < k; j += 8) {
-            const int id = pick_id[r][j];
-            if (id < e0 || id >= e0 + kPrepCols) continue;
-            // the first pick of an expert adds every pick of it
-            bool first = true;
-            float v = pick_v[r][j];
-            for (int i = 0; i < k; ++i) {
-                if (i == j || pick_id[r][i] != id) continue;
-                if (i < j) first = false;
-                else v += pick_v[r][i];
-            }
-            if (first) tile[r * kPrepStride + id - e0] += v;
-        }
-    }
-    __syncthreads();
-    for (int i = tid; i < kPrepRows * kPrepCols; i += kPrepBlock) {
-        const int r = i / kPrepCols, c = i - r * kPrepCols;
-        const int t = t0 + r, e = e0 + c;
-        if (t < T && e < E) d_logits[static_cast<size_t>(t) * E + e] = tile[r * kPrepStride + c];
-    }
-    if (row_bits && blockIdx.y == 0 && tid < kWave) {
-        const bool ok = tid < kPrepRows && t0 + tid < T && mask[t0 + tid] != 0;
-        const uint64_t b = ballot(ok);
-        if (tid < 2) row_bits[blockIdx.x * 2 + tid] = static_cast<uint32_t>(b >> (16 * tid)) & 0xFFFFu;
-    }
-    const int lane = tid & 63;
-    if (frag_h) {
-        const int ks_n = (E + kKStep - 1) / kKStep;
-        for (int f = tid / kWave; f < kPrepCols / kKStep; f += kPrepBlock / kWave) {
-            const int ks = e0 / kKStep + f;
-            if (ks >= ks_n) break;
-            float v[8];
+struct PrepArgs {
+    const float* d_topk_w;
+    const float* d_aux;
+    const float* logits;
+    const int32_t* ids;
+    const float* topk_w;
+    const uint8_t* mask;
+    int T, E, k, H;
+    float scale;
+    float* d_logits;
+    u32x4* frag_h;        // fragments with rows tokens, summed over experts (np_h planes)
+    int np_h;
+    u32x4* frag_w;        // with rows experts, summed over tokens (three planes)
+    uint32_t* row_bits;   // for every 16 tokens a word, one bit each, set for valid ones
+    uint32_t* zeros;
+    int tiles_t, tiles_e;   // blocks of the gradient; those behind them split rows
+    SplitArgs split[2];     // W and an FP32 input
+    long long split_blocks0;
+};
+
+__device__ __forceinline__ void split_rows(const SplitArgs& a, int H, long long block) {
+    const long long per_row = H / 4;
+    const long long quads = a.rows * per_row;
+    const size_t plane = static_cast<size_t>(a.rows) * H;
+    f32x4 v[kSplitQuads];
 #pragma unroll
-            for (int j = 0; j < 8; ++j) v[j] = tile[(lane & 31) * kPrepStride + f * kKStep + 8 * (lane >> 5) + j];
-            write_fragment(v, np_h, frag_h + (static_cast<size_t>(blockIdx.x) * ks_n + ks) * np_h * kWave + lane);
-        }
+    for (int q = 0; q < kSplitQuads; ++q) {
+        const long long i = (block * kSplitQuads + q) * kPrepBlock + threadIdx.x;
+        v[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (i < quads && (!a.mask || a.mask[i / per_row])) v[q] = reinterpret_cast<const f32x4*>(a.x)[i];
     }
-    if (frag_w) {
-        const int mt_n = (E + 31) / 32;
-        const size_t ks_n = 2 * static_cast<size_t>(gridDim.x);
-        for (int f = tid / kWave; f < 2 * (kPrepCols / 32); f += kPrepBlock / kWave) {
-            const int mt = e0 / 32 + (f >> 1), half = f & 1;
-            if (mt >= mt_n) break;
-            float v[8];
 #pragma unroll
-            for (int j = 0; j < 8; ++j)
-                v[j] = tile[(half * kKStep + 8 * (lane >> 5) + j) * kPrepStride + (f >> 1) * 32 + (lane & 31)];
-            write_fragment(v, 3, frag_w + (mt * ks_n + 2 * blockIdx.x + half) * 3 * kWave + lane);
-        }
+    for (int q = 0; q < kSplitQuads; ++q) {
+        const long long i = (block * kSplitQuads + q) * kPrepBlock + threadIdx.x;
+        if (i >= quads) break;
+        u32x2 o[3];
+        uint32_t x, y, z;
+        split_pair(v[q][0], v[q][1], x, y, z);
+        o[0][0] = x;
+        o[1][0] = y;
+        o[2][0] = z;
+        split_pair(v[q][2], v[q][3], x, y, z);
+        o[0][1] = x;
+        o[1][1] = y;
+        o[2][1] = z;
+#pragma unroll
+        for (int p = 0; p < 3; ++p)
+            if (p < a.np) reinterpret_cast<u32x2*>(a.planes + p * plane)[i] = o[p];
     }
 }
 
-// FP32 rows [rows,H] -> np BF16 planes [np][rows][H]; rows whose mask byte is
-// zero become zeros.
-__global__ __launch_bounds__(256) void split_rows_kernel(const float* __restrict__ x, const uint8_t* __restrict__ mask,
-                                                         int rows, int H, int np, uint16_t* __restrict__ planes) {
-    const long long quads = static_cast<long long>(rows) * (H / 4);
-    const size_t plane = static_cast<size_t>(rows) * H;
-    for (long long i = blockIdx.x * 256ll + threadIdx.x; i < quads; i += gridDim.x * 256ll) {
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (!mask || mask[i / (H / 4)]) v = reinterpret_cast<const float4*>(x)[i];
-        u32x2 q[3];
-        uint32_t a, b, c;
-        split_pair(v.x, v.y, a, b, c);
-        q[0][0] = a;
-        q[1][0] = b;
-        q[2][0] = c;
-        split_pair(v.z, v.w, a, b, c);
-        q[0][1] = a;
-        q[1][1] = b;
-        q[2][1] = c;
+// Block x + tiles_t y: tokens [32 x, +32), experts [128 y, +128); the blocks
+// behind them split W and an FP32 input into planes. Fragments of a matrix with
+// rows m and summation index c: [m / 32][c / 16][plane][lane], lane l holding
+// row l % 32, c = 8 (l / 32) .. +8; their values are scaled, d_logits is not.
+// d_aux may be d_logits: a block reads its tile before it writes it.
+__global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepArgs p) {
+    const int T = p.T, E = p.E, k = p.k;
+    const long long grad_blocks = static_cast<long long>(p.tiles_t) * p.tiles_e;
+    if (blockIdx.x >= grad_blocks) {
+        const long long b = blockIdx.x - grad_blocks;
+        if (b < p.split_blocks0) split_rows(p.split[0], p.H, b);
+        else split_rows(p.split[1], p.H, b - p.split_blocks0);
+        return;
+    }
+    __shared__ __attribute__((aligned(16))) float tile[kPrepRows * kPrepStride];
+    __shared__ int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
+    __shared__ float pick_v[kPrepRows][MOE_MAX_TOPK];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int by = static_cast<int>(blockIdx.x / p.tiles_t), bx = static_cast<int>(blockIdx.x - static_cast<long long>(by) * p.tiles_t);
+    const int t0 = bx * kPrepRows, e0 = by * kPrepCols;
+    if (p.zeros && blockIdx.x == 0)
+        for (int i = tid; i < static_cast<int>(kZeroBytes / 4); i += kPrepBlock) p.zeros[i] = 0;
+
+    const uint32_t valid = static_cast<uint32_t>(ballot(lane < kPrepRows && t0 + lane < T && p.mask[t0 + lane] != 0));
+    if (p.row_bits && by == 0 && tid < 2) p.row_bits[bx * 2 + tid] = valid >> (16 * tid) & 0xFFFFu;
+    // the picks' ids and weights: eight threads a token, up to four picks each
+    const int pr = tid >> 3, sub = tid & 7;
+    constexpr int kPicks = MOE_MAX_TOPK / 8;
+    int id[kPicks];
+    float w[kPicks], dw[kPicks], l[kPicks];
+    if (p.d_topk_w) {
 #pragma unroll
-        for (int p = 0; p < 3; ++p)
-            if (p < np) reinterpret_cast<u32x2*>(planes + p * plane)[i] = q[p];
+        for (int q = 0; q < kPicks; ++q) {
+            const int j = sub + 8 * q;
+            const size_t at = static_cast<size_t>(t0 + pr) * k + j;
+            id[q] = -1;
+            w[q] = dw[q] = l[q] = 0.f;
+            if (j < k && (valid >> pr & 1)) {
+                const int e = p.ids[at];
+                if (e >= 0 && e < E) {
+                    id[q] = e;
+                    w[q] = p.topk_w[at];
+                    dw[q] = p.d_topk_w[at];
+                }
+            }
+        }
+    }
+    // d_aux: piece i of the tile is row tid / 32 + 8 i, columns 4 (tid % 32) .. +4
+    const int col = e0 + 4 * (tid & 31);
+    f32x4 v[kPrepLoads];
+#pragma unroll
+    for (int i = 0; i < kPrepLoads; ++i) {
+        const int r = (tid >> 5) + 8 * i;
+        v[i] = f32x4{0.f, 0.f, 0.f, 0.f};
+        if (p.d_aux && (valid >> r & 1)) {
+            const float* src = p.d_aux + static_cast<size_t>(t0 + r) * E + col;
+            if (col + 4 <= E) v[i] = *reinterpret_cast<const f32x4_any*>(src);
+            else
+                for (int c = 0; c < 4; ++c)
+                    if (col + c < E) v[i][c] = src[c];
+        }
+    }
+    if (p.d_topk_w) {
+        float s = 0.f;
+#pragma unroll
+        for (int q = 0; q < kPicks; ++q) {
+            s = __builtin_fmaf(w[q], dw[q], s);
+            const bool here = id[q] >= e0 && id[q] < e0 + kPrepCols;
+            if (here) l[q] = p.logits[static_cast<size_t>(t0 + pr) * E + id[q]];
+        }
+        s = group_sum(s, 8);
+#pragma unroll
+        for (int q = 0; q < kPicks; ++q) {
+            const int j = sub + 8 * q;
+            if (j >= k) continue;
+            pick_id[pr][j] = id[q];
+            pick_v[pr][j] = w[q] * (dw[q] - s) / (1.f + expf(l[q]));   // 1 - sigmoid(l) = 1 / (1 + exp(l))
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < kPrepLoads; ++i)
+        *reinterpret_cast<f32x4*>(&tile[((tid >> 5) + 8 * i) * kPrepStride + 4 * (tid & 31)]) = v[i];
+    __syncthreads();
+    if (p.d_topk_w) {
+#pragma unroll
+        for (int q = 0; q < kPicks; ++q) {
+            if (id[q] < e0 || id[q] >= e0 + kPrepCols) continue;
+            // the first pick of an expert adds every pick of it
+            const int j = sub + 8 * q;
+            bool first = true;
+            float sum = pick_v[pr][j];
+            for (int i = 0; i < k; ++i) {
+                if (i == j || pick_id[pr][i] != id[q]) continue;
+                if (i < j) first = false;
+                else sum += pick_v[pr][i];
+            }
+            if (first) tile[pr * kPrepStride + id[q] - e0] += sum;
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int i = 0; i < kPrepLoads; ++i) {
+        const int r = (tid >> 5) + 8 * i;
+        if (t0 + r >= T) break;
+        const f32x4 o = *reinterpret_cast<const f32x4*>(&tile[r * kPrepStride + 4 * (tid & 31)]);
+        float* dst = p.d_logits + static_cast<size_t>(t0 + r) * E + col;
+        if (col + 4 <= E) *reinterpret_cast<f32x4_any*>(dst) = o;
+        else
+            for (int c = 0; c < 4; ++c)
+                if (col + c < E) dst[c] = o[c];
+    }
+    if (p.frag_h) {
+        const int ks_n = (E + kKStep - 1) / kKStep;
+#pragma unroll
+        for (int q = 0; q < kPrepCols / kKStep / 4; ++q) {
+            const int f = tid / kWave + 4 * q;
+            const int ks = e0 / kKStep + f;
+            if (ks >= ks_n) break;
+            const f32x4* src = reinterpret_cast<const f32x4*>(&tile[(lane & 31) * kPrepStride + f * kKStep + 8 * (lane >> 5)]);
+            const f32x4 lo = src[0] * p.scale, hi = src[1] * p.scale;
+            const float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
+            write_fragment(x, p.np_h, p.frag_h + (static_cast<size_t>(bx) * ks_n + ks) * p.np_h * kWave + lane);
+        }
+    }
+    if (p.frag_w) {
+        const int mt_n = (E + 31) / 32;
+        const size_t ks_n = 2 * static_cast<size_t>(p.tiles_t);
+#pragma unroll
+        for (int q = 0; q < kPrepCols / 32 / 2; ++q) {
+            const int f = tid / kWave + 4 * q;
+            const int mt = e0 / 32 + (f >> 1), half = f & 1;
+            if (mt >= mt_n) break;
+            float x[8];
+#pragma unroll
+            for (int j = 0; j < 8; ++j)
+                x[j] = tile[(half * kKStep + 8 * (lane >> 5) + j) * kPrepStride + (f >> 1) * 32 + (lane & 31)] * p.scale;
+            write_fragment(x, 3, p.frag_w + (mt * ks_n + 2 * bx + half) * 3 * kWave + lane);
+        }
     }
 }
 
@@ -207,189 +282,316 @@ __device__ __forceinline__ void wait_vmcnt() {
     __builtin_amdgcn_s_waitcnt((N & 0xF) | ((N >> 4) << 14) | (0x7 << 4) | (0xF << 8));
 }
 
-// Block tile 64 WM x 128 WN, one wave per 64 x 128 (2 x 4 accumulators of
-// v_mfma_f32_32x32x16_bf16). Every K-step's A fragments and B rows go through
-// a ring of LDS stages filled LOOK steps ahead by direct-to-LDS loads of 1 KB,
-// the same number by every wave, so that waiting for all but the newest
-// (LOOK - 1) groups means the step's own group has landed.
-template <int NA, int NB, int WM, int WN>
+__device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4)); }
+
+// Block tile 64 WM x 256, 2 WM waves of 64 x 128 (2 x 4 accumulators of
+// v_mfma_f32_32x32x16_bf16).
+//
+// Pipeline: every K-step's A fragments and B rows go through a ring of SETS LDS
+// stages filled by direct-to-LDS loads of 1 KB, the same number by every wave;
+// loads complete in issue order, so waiting for all but the newest (SETS - 2)
+// groups means the next step's has landed. Step g issues the loads of step
+// g + SETS into the stage that all waves have read, reads step g + 1's operands
+// from LDS into the other register set and multiplies step g's, so that
+// neither kind of load is waited for beside idle matrix cores. Blocks are
+// persistent: the steps of a block's tiles form one sequence, and the loads of
+// the next tile are in flight while the results of the last one are stored.
+template <int NA, int NB, int WM>
 struct ProductShape {
-    static constexpr int WAVES = WM * WN;
+    static constexpr int WAVES = 2 * WM;
     static constexpr int BLOCK = WAVES * kWave;
-    static constexpr int BM = 64 * WM, BN = 128 * WN;
-    static constexpr int LA = 2 * WM * NA;            // 1 KB loads of A per step
-    static constexpr int LB = NB * 4 * WN;            // and of B: NB planes of 16 rows
-    static constexpr int LOADS = (LA + LB) / WAVES;   // per wave
+    static constexpr int BM = 64 * WM, BN = 256;
+    static constexpr int LA = 2 * WM * NA;      // 1 KB loads of A per step: NA per wave
+    static constexpr int LB = 8 * NB;           // and of B: NB planes of 16 rows
+    static constexpr int WB = LB / WAVES;       // per wave
+    static constexpr int LOADS = NA + WB;
     static constexpr int STAGE = (LA + LB) * kFrag;
-    static constexpr int SETS = 4 * STAGE <= 136 * 1024 ? 4 : 3;
-    static constexpr int LOOK = SETS - 1;
+    static constexpr int SETS = 4 * STAGE <= 144 * 1024 ? 4 : 3;
     static constexpr size_t LDS = static_cast<size_t>(SETS) * STAGE;
-    static_assert((LA + LB) % WAVES == 0, "every wave issues the same number of loads");
+    static constexpr int STORES = 32;           // of a wave per tile
+    static_assert(LB % WAVES == 0, "every wave issues the same number of loads");
     static_assert(LDS <= 160 * 1024, "LDS of a CU");
-    static_assert(BN * 2 <= static_cast<int>(kZeroBytes) && BN <= 512, "a row of zeros, a row per load");
+    static_assert((SETS - 2) * LOADS + STORES < 64, "vmcnt range");
+    static_assert(BN * 2 <= static_cast<int>(kZeroBytes), "a row of zeros");
 };
 
 struct ProductArgs {
     const u32x4* a;            // fragments [m / 32][K / 16][NA][64]
     const uint16_t* b;         // [NB][rows][n]
     size_t b_plane;            // elements between planes
-    const uint32_t* row_bits;  // valid rows of each K-step, or NULL
+    const uint32_t* row_bits;  // valid rows of each K-step; NULL: those below `rows`
     const uint16_t* zeros;     // kZeroBytes of zeros
-    float scale;
     int m, n, rows, a_steps;   // a_steps: K-steps the fragments hold (>= steps)
     int steps, split_steps;    // K-steps in all, and of one split
     int tiles_m, tiles_n, nsplit;
     void* c;                   // [m,n]; with nsplit > 1 FP32 partial sums [nsplit,m,n]
 };
 
-template <int NA, int NB, int WM, int WN, bool BF16_OUT>
-__global__ __launch_bounds__(WM* WN* kWave) void product_kernel(const ProductArgs p) {
-    using S = ProductShape<NA, NB, WM, WN>;
+// Operands of one K-step as a wave reads them from LDS: its A fragments, and
+// eight rows of four columns of B.
+template <int NA, int NB>
+struct StepOperands {
+    bf16x8_t a[NA][2];
+    u32x2 b[NB][8];
+};
+
+template <int NA, int NB, int WM, bool BF16_OUT>
+__global__ __launch_bounds__(2 * WM * kWave, WM == 4 ? 2 : 1) void product_kernel(
+    const ProductArgs p) {
+#ifdef __HIP_DEVICE_COMPILE__   // the host pass only needs the kernel's handle
+    using S = ProductShape<NA, NB, WM>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
-    // the blocks of an XCD (every eighth) take consecutive tiles: row tiles
-    // of one column tile first, then column tiles, then K-splits
+    // The blocks of an XCD (every eighth) take a run of consecutive tiles: row
+    // tiles of one column tile first, then column tiles, then K-splits.
     const int total = p.tiles_m * p.tiles_n * p.nsplit;
-    const int per_xcd = static_cast<int>(gridDim.x) / 8;
-    const int idx = static_cast<int>(blockIdx.x % 8) * per_xcd + static_cast<int>(blockIdx.x / 8);
-    if (idx >= total) return;
-    const int split = idx / (p.tiles_m * p.tiles_n);
-    const int tile = idx - split * (p.tiles_m * p.tiles_n);
-    const int n_tile = tile / p.tiles_m, m_tile = tile - n_tile * p.tiles_m;
-    const int m0 = m_tile * S::BM, n0 = n_tile * S::BN;
-    const int s_beg = split * p.split_steps;
-    const int nst = min(p.steps, s_beg + p.split_steps) - s_beg;
+    const int per_xcd = (total + 7) / 8;
+    const int xcd = static_cast<int>(blockIdx.x % 8);
+    const int run_end = min(total, (xcd + 1) * per_xcd);
+    const int stride = static_cast<int>(gridDim.x) / 8;
+    const int first = xcd * per_xcd + static_cast<int>(blockIdx.x / 8);
+    if (first >= run_end) return;
 
     const int lane = __lane_id();
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    const int wm = wave / WN, wn = wave % WN;
-
-    f32x16_t acc[2][4];
-#pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-        for (int j = 0; j < 4; ++j)
-#pragma unroll
-            for (int i = 0; i < 16; ++i) acc[mi][j][i] = 0.f;
-
+    const int wm = wave >> 1, wn = wave & 1;
     const int m_last = (p.m + 31) / 32 - 1;
-    // a B load covers 512 / BN rows; this lane's row within them and columns
-    constexpr int kRowsPerLoad = 512 / S::BN;
-    const int b_row = lane / (S::BN / 8);
-    const int b_col = (lane % (S::BN / 8)) * 8;
-    const int b_src_col = min(n0 + b_col, p.n - 8);   // columns past n repeat the last ones (never stored)
+    const int per_split = p.tiles_m * p.tiles_n;
 
-    auto issue = [&](int step, int set, uint32_t bits) {
-        char* base = lds + set * S::STAGE;
-        const int ks = s_beg + step;
+    // ---- the loads' cursor: tile l_tile, K-step l_ks up to l_end
+    int l_tile = first, l_ks = 0, l_end = 0;
+    // wave-uniform parts of the sources (scalar registers); the lanes' offsets
+    // are the same for every load of a tile
+    const u32x4* a_src[NA];
+    const uint16_t* b_src[S::WB];
+    const int b_row = lane >> 5, b_col = (lane & 31) * 8;   // a B load covers two rows of 256 columns
+    int b_lane = 0;
+    auto load_tile = [&]() {
+        const int split = l_tile / per_split;
+        const int tile = l_tile - split * per_split;
+        const int n_tile = tile / p.tiles_m, m_tile = tile - n_tile * p.tiles_m;
+        l_ks = split * p.split_steps;
+        l_end = min(p.steps, l_ks + p.split_steps);
 #pragma unroll
-        for (int i = 0; i < S::LOADS; ++i) {
-            const int l = wave + i * S::WAVES;   // this load of the stage
-            const void* src;
-            if (l < S::LA) {
-                const int mt = min(m0 / 32 + l / NA, m_last);
-                src = p.a + ((static_cast<size_t>(mt) * p.a_steps + ks) * NA + l % NA) * kWave + lane;
-            } else {
-                const int lb = l - S::LA;
-                const int pl = lb / (4 * WN);
-                const int r = (lb - pl * 4 * WN) * kRowsPerLoad + b_row;
-                const int row = ks * kKStep + r;
-                const bool ok = row < p.rows && (bits >> r & 1);
-                src = ok ? p.b + pl * p.b_plane + static_cast<size_t>(row) * p.n + b_src_col : p.zeros + b_col;
-            }
-            __builtin_amdgcn_global_load_lds(src, base + l * kFrag, 16, 0, 0);
+        for (int i = 0; i < NA; ++i) {
+            const int l = wave + i * S::WAVES;
+            const int mt = min(m_tile * (S::BM / 32) + l / NA, m_last);
+            a_src[i] = p.a + ((static_cast<size_t>(mt) * p.a_steps + l_ks) * NA + l % NA) * kWave;
+        }
+        const int n0 = n_tile * S::BN;
+        b_lane = b_row * p.n + min(b_col, p.n - 8 - n0);   // columns past n repeat the last ones (never stored)
+#pragma unroll
+        for (int i = 0; i < S::WB; ++i) {
+            const int l = wave + i * S::WAVES;
+            const size_t row = static_cast<size_t>(l_ks) * kKStep + (l & 7) * 2;
+            b_src[i] = p.b + (l >> 3) * p.b_plane + row * p.n + n0;
         }
     };
-    // through the constant address space: a scalar load, which the wait for the
-    // vector loads does not count
+    // through the constant address space: a scalar load, which the waits for the
+    // vector loads do not count
     const auto* bits_at = (const __attribute__((address_space(4))) uint32_t*)(p.row_bits);
-    auto bits_of = [&](int step) { return p.row_bits ? bits_at[s_beg + step] : 0xFFFFu; };
-
+    auto bits_of = [&](int ks) -> uint32_t {
+        if (p.row_bits) return bits_at[ks];
+        const int left = p.rows - ks * kKStep;
+        return left >= kKStep ? 0xFFFFu : (1u << left) - 1u;
+    };
+    uint32_t l_bits;
+    auto issue = [&](int set) {
+        char* base = lds + set * S::STAGE;
 #pragma unroll
-    for (int s = 0; s < S::LOOK; ++s) {
-        issue(min(s, nst - 1), s, bits_of(min(s, nst - 1)));
-        __builtin_amdgcn_sched_barrier(0);
-    }
-    uint32_t next_bits = bits_of(min(S::LOOK, nst - 1));
-    int set = 0;
-    for (int s = 0; s < nst; ++s) {
-        __builtin_amdgcn_sched_barrier(0);
-        wait_vmcnt<(S::LOOK - 1) * S::LOADS>();   // step s's loads have landed
-        __builtin_amdgcn_s_barrier();             // ... in every wave, and step s - 1's stage is free
-        __builtin_amdgcn_sched_barrier(0);
-        const int refill = set == 0 ? S::SETS - 1 : set - 1;
-        // past the last step the last one's loads are repeated, into a stage
-        // that is not read again
-        issue(min(s + S::LOOK, nst - 1), refill, next_bits);
-        next_bits = bits_of(min(s + 1 + S::LOOK, nst - 1));
-        __builtin_amdgcn_sched_barrier(0);
-        const char* base = lds + set * S::STAGE;
-        bf16x8_t a[NA][2];
+        for (int i = 0; i < NA; ++i)
+            __builtin_amdgcn_global_load_lds(a_src[i] + lane, base + (wave + i * S::WAVES) * kFrag, 16, 0, 0);
+        if (l_bits == 0xFFFFu) {
 #pragma unroll
-        for (int pl = 0; pl < NA; ++pl)
+            for (int i = 0; i < S::WB; ++i)
+                __builtin_amdgcn_global_load_lds(b_src[i] + b_lane, base + (S::LA + wave + i * S::WAVES) * kFrag, 16, 0,
+                                                 0);
+        } else {
 #pragma unroll
-            for (int mi = 0; mi < 2; ++mi)
-                a[pl][mi] = *reinterpret_cast<const bf16x8_t*>(base + ((wm * 2 + mi) * NA + pl) * kFrag + lane * 16);
-        bf16x8_t b[NB][4];
+            for (int i = 0; i < S::WB; ++i) {
+                const int l = wave + i * S::WAVES;
+                const bool ok = l_bits >> ((l & 7) * 2 + b_row) & 1;
+                const uint16_t* src = ok ? b_src[i] + b_lane : p.zeros + b_col;
+                __builtin_amdgcn_global_load_lds(src, base + (S::LA + l) * kFrag, 16, 0, 0);
+            }
+        }
+    };
+    // on to the next step, or the next tile's first; behind the last tile the
+    // last step is loaded again, into stages that nobody uses
+    auto advance = [&]() {
+        if (l_ks + 1 < l_end) {
+            ++l_ks;
 #pragma unroll
-        for (int pl = 0; pl < NB; ++pl) {
-            const char* src = base + S::LA * kFrag + (pl * kKStep + 8 * (lane >> 5)) * (S::BN * 2) + wn * 256 +
+            for (int i = 0; i < NA; ++i) a_src[i] += NA * kWave;
+#pragma unroll
+            for (int i = 0; i < S::WB; ++i) b_src[i] += static_cast<size_t>(kKStep) * p.n;
+        } else if (l_tile + stride < run_end) {
+            l_tile += stride;
+            load_tile();
+        }
+        l_bits = bits_of(l_ks);
+    };
+    // Piece i of a step's operands: first the pairs of B's rows, then the A
+    // fragments.
+    constexpr int kPieces = 4 * NB + 2 * NA;
+    auto read_piece = [&](const char* base, StepOperands<NA, NB>& f, int i) {
+        if (i < 4 * NB) {
+            const int pl = i >> 2, r = (i & 3) * 2;
+            const char* src = base + S::LA * kFrag + (pl * kKStep + 8 * (lane >> 5) + r) * (S::BN * 2) + wn * 256 +
                               (lane & 31) * 8;
-            u32x2 r[8];
+            f.b[pl][r] = *reinterpret_cast<const u32x2*>(src);
+            f.b[pl][r + 1] = *reinterpret_cast<const u32x2*>(src + S::BN * 2);
+        } else if (i < kPieces) {
+            const int mi = (i - 4 * NB) / NA, pl = (i - 4 * NB) % NA;
+            f.a[pl][mi] = *reinterpret_cast<const bf16x8_t*>(base + ((wm * 2 + mi) * NA + pl) * kFrag + lane * 16);
+        }
+    };
+
+    f32x16_t acc[2][4];
+    auto clear = [&]() {
 #pragma unroll
-            for (int i = 0; i < 8; ++i) r[i] = *reinterpret_cast<const u32x2*>(src + i * (S::BN * 2));
+        for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) acc[mi][j][i] = 0.f;
+    };
+    // The products of planes (pa, pb) with pa + pb < max(NA, NB) of step f, and
+    // the reads of the next step's operands spread between them, two pieces to
+    // four MFMAs: issued in a run they would keep the matrix cores waiting for
+    // the LDS queue.
+    auto multiply = [&](const StepOperands<NA, NB>& f, const char* base, StepOperands<NA, NB>& next) {
+        constexpr int PMAX = NA > NB ? NA : NB;
+        int piece = 0;
+#pragma unroll
+        for (int pb = 0; pb < NB; ++pb) {
+            bf16x8_t b[4];
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 u32x4 v;
 #pragma unroll
                 for (int d = 0; d < 4; ++d)
-                    v[d] = __builtin_amdgcn_perm(r[2 * d + 1][j >> 1], r[2 * d][j >> 1],
+                    v[d] = __builtin_amdgcn_perm(f.b[pb][2 * d + 1][j >> 1], f.b[pb][2 * d][j >> 1],
                                                  j & 1 ? 0x07060302u : 0x05040100u);
-                b[pl][j] = __builtin_bit_cast(bf16x8_t, v);
+                b[j] = __builtin_bit_cast(bf16x8_t, v);
             }
-        }
-        // the products of planes (pa, pb) with pa + pb < max(NA, NB)
-        constexpr int PMAX = NA > NB ? NA : NB;
 #pragma unroll
-        for (int pa = 0; pa < NA; ++pa)
-#pragma unroll
-            for (int pb = 0; pb < NB; ++pb) {
+            for (int pa = 0; pa < NA; ++pa) {
                 if (pa + pb >= PMAX) continue;
 #pragma unroll
-                for (int mi = 0; mi < 2; ++mi)
+                for (int mi = 0; mi < 2; ++mi) {
+                    read_piece(base, next, piece);
+                    read_piece(base, next, piece + 1);
+                    piece += 2;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
-                        acc[mi][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(a[pa][mi], b[pb][j], acc[mi][j], 0, 0, 0);
+                        acc[mi][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(f.a[pa][mi], b[j], acc[mi][j], 0, 0, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
             }
-        set = set + 1 == S::SETS ? 0 : set + 1;
-    }
-    wait_vmcnt<0>();   // the repeated loads, before the block's LDS is given away
+        }
+    };
 
-    // lane: columns 4 (lane % 32) + j of the wave's 128, rows
-    // 8 (i / 4) + 4 (lane / 32) + i % 4 of each 32
-    const int col = n0 + wn * 128 + 4 * (lane & 31);
-    if (col >= p.n) return;
-    const size_t part = p.nsplit > 1 ? static_cast<size_t>(split) * p.m : 0;
-    const float scale = p.nsplit > 1 ? 1.f : p.scale;
-#pragma unroll
-    for (int mi = 0; mi < 2; ++mi)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int row = m0 + (wm * 2 + mi) * 32 + 8 * (i >> 2) + 4 * (lane >> 5) + (i & 3);
-            if (row >= p.m) continue;
-            const float v0 = acc[mi][0][i] * scale, v1 = acc[mi][1][i] * scale;
-            const float v2 = acc[mi][2][i] * scale, v3 = acc[mi][3][i] * scale;
+    // Stores the tile's results; returns the stores that are certainly behind
+    // the loads in flight (none at the matrix' edges, where some are skipped).
+    // lane: columns 4 (lane % 32) + j of the wave's 128, rows 8 (i / 4) +
+    // 4 (lane / 32) + i % 4 of each 32
+    auto store_tile = [&](int t) {
+        const int split = t / per_split;
+        const int tile = t - split * per_split;
+        const int n_tile = tile / p.tiles_m, m_tile = tile - n_tile * p.tiles_m;
+        const int m0 = m_tile * S::BM + wm * 64 + 4 * (lane >> 5);
+        const int col = n_tile * S::BN + wn * 128 + 4 * (lane & 31);
+        const size_t part = p.nsplit > 1 ? static_cast<size_t>(split) * p.m : 0;
+        auto put = [&](int mi, int i) {
+            const int row = m0 + mi * 32 + 8 * (i >> 2) + (i & 3);
             const size_t at = (part + row) * p.n + col;
+            const float v0 = acc[mi][0][i], v1 = acc[mi][1][i], v2 = acc[mi][2][i], v3 = acc[mi][3][i];
             if constexpr (BF16_OUT)
                 *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.c) + at) =
                     u32x2{cvt_pk_bf16(v0, v1), cvt_pk_bf16(v2, v3)};
             else
                 *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) = make_float4(v0, v1, v2, v3);
+        };
+        const bool whole = (m_tile + 1) * S::BM <= p.m && (n_tile + 1) * S::BN <= p.n;
+        if (whole) {
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                for (int i = 0; i < 16; ++i) put(mi, i);
+            return true;
         }
+        if (col < p.n) {
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    if (m0 + mi * 32 + 8 * (i >> 2) + (i & 3) < p.m) put(mi, i);
+        }
+        return false;
+    };
+
+    // ---- the tile being computed
+    int c_tile = first;
+    auto tile_steps = [&](int t) {
+        const int beg = t / per_split * p.split_steps;
+        return min(p.steps, beg + p.split_steps) - beg;
+    };
+    int left = tile_steps(c_tile);
+    int behind = 0;   // steps for which the last tile's stores are behind the loads waited for
+
+    load_tile();
+    l_bits = bits_of(l_ks);
+#pragma unroll
+    for (int s = 0; s < S::SETS; ++s) {
+        issue(s);
+        advance();
+        __builtin_amdgcn_sched_barrier(0);
+    }
+    StepOperands<NA, NB> f0, f1;
+    wait_vmcnt<(S::SETS - 1) * S::LOADS>();
+    __builtin_amdgcn_s_barrier();
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int i = 0; i < kPieces; ++i) read_piece(lds, f0, i);
+    clear();
+    int set = 0;
+    // one step: f holds its operands, g takes the next step's; false behind the
+    // last step of the last tile
+    auto step = [&](const StepOperands<NA, NB>& f, StepOperands<NA, NB>& g) {
+        __builtin_amdgcn_sched_barrier(0);
+        // the next step's loads have landed ...
+        if (behind > 0) {
+            wait_vmcnt<(S::SETS - 2) * S::LOADS + S::STORES>();
+            --behind;
+        } else {
+            wait_vmcnt<(S::SETS - 2) * S::LOADS>();
+        }
+        wait_lgkmcnt0();                // ... this step's operands are in registers ...
+        __builtin_amdgcn_s_barrier();   // ... in every wave: its stage is free
+        __builtin_amdgcn_sched_barrier(0);
+        issue(set);
+        set = set + 1 == S::SETS ? 0 : set + 1;
+        __builtin_amdgcn_sched_barrier(0);
+        multiply(f, lds + set * S::STAGE, g);
+        advance();
+        if (--left > 0) return true;
+        __builtin_amdgcn_sched_barrier(0);
+        behind = store_tile(c_tile) ? S::SETS - 1 : 0;
+        __builtin_amdgcn_sched_barrier(0);
+        c_tile += stride;
+        if (c_tile >= run_end) return false;
+        left = tile_steps(c_tile);
+        clear();
+        return true;
+    };
+    while (step(f0, f1) && step(f1, f0)) {}
+    wait_vmcnt<0>();   // loads in flight, before the block's LDS is given away
+#endif
 }
 
-// out = scale * (sum of n partial arrays, in order); zeros without any.
+// The sum of n partial arrays, in order; zeros without any.
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float4* __restrict__ parts, int n, long long quads,
-                                                        float scale, float4* __restrict__ out) {
+                                                        float4* __restrict__ out) {
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < quads; i += gridDim.x * 256ll) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -400,7 +602,7 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float4* __restrict
             s.z += v.z;
             s.w += v.w;
         }
-        out[i] = make_float4(s.x * scale, s.y * scale, s.z * scale, s.w * scale);
+        out[i] = s;
     }
 }
 
@@ -413,12 +615,13 @@ struct ProductPlan {
     int tiles_m, tiles_n, steps, nsplit, split_steps;
 };
 
-// Row tiles of 64, 128 or 256 as the rows need. K is split where that shortens
+// Row tiles of 64, 128 or 256 as the rows need (at most 128 with three planes of
+// each factor, whose operands take twice the registers). K is split where that shortens
 // the product more than the partial sums, written and read once, cost: a step
 // of a 256-row tile is taken as 1 us, partial sums as 4 TB/s.
-inline ProductPlan plan_product(int m, int n, long long k, bool may_split) {
+inline ProductPlan plan_product(int m, int n, long long k, bool f32, bool may_split) {
     ProductPlan p;
-    p.wm = m <= 64 ? 1 : m <= 128 ? 2 : 4;
+    p.wm = m <= 64 ? 1 : m <= 128 || f32 ? 2 : 4;
     p.tiles_m = ceil_div(m, 64 * p.wm);
     p.tiles_n = ceil_div(n, 256);
     p.steps = ceil_div(k, kKStep);
@@ -426,7 +629,7 @@ inline ProductPlan plan_product(int m, int n, long long k, bool may_split) {
     p.split_steps = p.steps;
     if (!may_split) return p;
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    const int slots = p.wm == 4 ? 256 : 512;   // blocks resident at once
+    const int slots = p.wm == 1 && !f32 ? 512 : 256;   // blocks resident at once
     double best = 0;
     for (int ns = 1; ns <= 32 && (ns == 1 || p.steps / ns >= 8); ++ns) {
         const int each = ceil_div(p.steps, ns);
@@ -458,8 +661,8 @@ inline RouteBackwardPlan plan_route_backward(int T, int H, int E, int dtype) {
     RouteBackwardPlan p;
     const bool f32 = dtype == MOE_DTYPE_F32;
     p.np_h = f32 ? 3 : 2;
-    p.h = plan_product(T, H, E, false);
-    p.w = plan_product(E, H, T, true);
+    p.h = plan_product(T, H, E, f32, false);
+    p.w = plan_product(E, H, T, f32, true);
     const size_t t32 = ceil_div(T, 32), e16 = ceil_div(E, 16), e32 = ceil_div(E, 32);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -480,10 +683,13 @@ inline RouteBackwardPlan plan_route_backward(int T, int H, int E, int dtype) {
 
 template <int NA, int NB, int WM, bool BF16_OUT>
 int launch_product_as(const ProductArgs& a, void* stream) {
-    using S = ProductShape<NA, NB, WM, 2>;
+    using S = ProductShape<NA, NB, WM>;
     const long long total = static_cast<long long>(a.tiles_m) * a.tiles_n * a.nsplit;
-    return launch(product_kernel<NA, NB, WM, 2, BF16_OUT>, dim3(8 * ceil_div(total, 8)), dim3(S::BLOCK), S::LDS,
-                  stream, a);
+    // one resident grid of persistent blocks, a multiple of the XCDs
+    const int most = device_cu_count() * (2 * S::LDS <= 160 * 1024 ? 2 : 1) / 8 * 8;
+    const long long grid = 8ll * ceil_div(total, 8);
+    return launch(product_kernel<NA, NB, WM, BF16_OUT>, dim3(static_cast<unsigned>(grid < most ? grid : most)),
+                  dim3(S::BLOCK), S::LDS, stream, a);
 }
 
 template <int NA, int NB, bool BF16_OUT>
@@ -493,9 +699,11 @@ int launch_product(const ProductPlan& p, ProductArgs a, void* stream) {
     a.tiles_m = p.tiles_m;
     a.tiles_n = p.tiles_n;
     a.nsplit = p.nsplit;
-    return p.wm == 1   ? launch_product_as<NA, NB, 1, BF16_OUT>(a, stream)
-           : p.wm == 2 ? launch_product_as<NA, NB, 2, BF16_OUT>(a, stream)
-                       : launch_product_as<NA, NB, 4, BF16_OUT>(a, stream);
+    if (p.wm == 1) return launch_product_as<NA, NB, 1, BF16_OUT>(a, stream);
+    if constexpr (NB == 3) return launch_product_as<NA, NB, 2, BF16_OUT>(a, stream);
+    else
+        return p.wm == 2 ? launch_product_as<NA, NB, 2, BF16_OUT>(a, stream)
+                         : launch_product_as<NA, NB, 4, BF16_OUT>(a, stream);
 }
 
 }  // namespace
@@ -528,7 +736,7 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         return dim3(static_cast<unsigned>(g < 2048 ? g : 2048));
     };
     if (T == 0)   // no token: the weight's gradient is zero
-        return d_W ? launch(sum_parts_kernel, grid_of(w_quads), dim3(256), 0, stream, nullptr, 0, w_quads, 0.f,
+        return d_W ? launch(sum_parts_kernel, grid_of(w_quads), dim3(256), 0, stream, nullptr, 0, w_quads,
                             reinterpret_cast<float4*>(d_W))
                    : MOE_OK;
     if (!token_mask || !d_logits || (!d_topk_w && !d_aux)) return MOE_ERR_NULL_ARG;
@@ -543,26 +751,49 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         if (!workspace || workspace_bytes < p.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
             return MOE_ERR_WORKSPACE;
     }
-    auto* frag_h = d_hidden ? reinterpret_cast<u32x4*>(ws + p.frag_h) : nullptr;
-    auto* frag_w = d_W ? reinterpret_cast<u32x4*>(ws + p.frag_w) : nullptr;
-    auto* bits = d_W ? reinterpret_cast<uint32_t*>(ws + p.bits) : nullptr;
-    auto* zeros = logits_in ? nullptr : reinterpret_cast<uint32_t*>(ws + p.zeros);
-    int st = launch(logits_gradient_kernel, dim3(ceil_div(T, kPrepRows), ceil_div(E, kPrepCols)), dim3(kPrepBlock), 0,
-                    stream, d_topk_w, d_aux, logits, topk_ids, topk_w, token_mask, T, E, k, d_logits, frag_h, p.np_h,
-                    frag_w, bits, zeros);
+    PrepArgs g{};
+    g.d_topk_w = d_topk_w;
+    g.d_aux = d_aux;
+    g.logits = logits;
+    g.ids = topk_ids;
+    g.topk_w = topk_w;
+    g.mask = token_mask;
+    g.T = T;
+    g.E = E;
+    g.k = k;
+    g.H = H;
+    g.scale = scale;
+    g.d_logits = d_logits;
+    g.frag_h = d_hidden ? reinterpret_cast<u32x4*>(ws + p.frag_h) : nullptr;
+    g.np_h = p.np_h;
+    g.frag_w = d_W ? reinterpret_cast<u32x4*>(ws + p.frag_w) : nullptr;
+    g.row_bits = d_W ? reinterpret_cast<uint32_t*>(ws + p.bits) : nullptr;
+    g.zeros = logits_in ? nullptr : reinterpret_cast<uint32_t*>(ws + p.zeros);
+    g.tiles_t = ceil_div(T, kPrepRows);
+    g.tiles_e = ceil_div(E, kPrepCols);
+    auto* w_planes = reinterpret_cast<uint16_t*>(ws + p.w_planes);
+    auto* x_planes = reinterpret_cast<uint16_t*>(ws + p.x_planes);
+    long long blocks[2] = {0, 0};
+    if (d_hidden) {
+        g.split[0] = SplitArgs{W, nullptr, E, p.np_h, w_planes};
+        blocks[0] = ceil_div(w_quads, kSplitQuads * kPrepBlock);
+    }
+    if (d_W && f32) {
+        g.split[1] = SplitArgs{static_cast<const float*>(hidden), token_mask, T, 3, x_planes};
+        blocks[1] = ceil_div(static_cast<long long>(T) * H / 4, kSplitQuads * kPrepBlock);
+    }
+    g.split_blocks0 = blocks[0];
+    const long long grid = static_cast<long long>(g.tiles_t) * g.tiles_e + blocks[0] + blocks[1];
+    if (grid >= (1ll << 31)) return MOE_ERR_BAD_SHAPE;
+    int st = launch(logits_gradient_kernel, dim3(static_cast<unsigned>(grid)), dim3(kPrepBlock), 0, stream, g);
     if (st != MOE_OK) return st;
     ProductArgs a{};
-    a.zeros = reinterpret_cast<const uint16_t*>(zeros);
-    a.scale = scale;
+    a.zeros = reinterpret_cast<const uint16_t*>(g.zeros);
     a.n = H;
     if (d_hidden) {
-        auto* planes = reinterpret_cast<uint16_t*>(ws + p.w_planes);
-        st = launch(split_rows_kernel, grid_of(w_quads), dim3(256), 0, stream, W, nullptr, E, H, p.np_h, planes);
-        if (st != MOE_OK) return st;
-        a.a = frag_h;
-        a.b = planes;
+        a.a = g.frag_h;
+        a.b = w_planes;
         a.b_plane = static_cast<size_t>(E) * H;
-        a.row_bits = nullptr;
         a.m = T;
         a.rows = E;
         a.a_steps = ceil_div(E, kKStep);
@@ -571,30 +802,25 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         if (st != MOE_OK) return st;
     }
     if (d_W) {
-        a.a = frag_w;
+        a.a = g.frag_w;
         a.m = E;
         a.rows = T;
-        a.a_steps = 2 * ceil_div(T, 32);
+        a.a_steps = 2 * g.tiles_t;
         a.c = p.w.nsplit > 1 ? static_cast<void*>(ws + p.parts) : static_cast<void*>(d_W);
-        if (f32) {
-            auto* planes = reinterpret_cast<uint16_t*>(ws + p.x_planes);
-            st = launch(split_rows_kernel, grid_of(static_cast<long long>(T) * H / 4), dim3(256), 0, stream,
-                        static_cast<const float*>(hidden), token_mask, T, H, 3, planes);
-            if (st != MOE_OK) return st;
-            a.b = planes;
+        if (f32) {   // the planes hold zeros for invalid tokens
+            a.b = x_planes;
             a.b_plane = static_cast<size_t>(T) * H;
-            a.row_bits = nullptr;   // the planes hold zeros for invalid tokens
             st = launch_product<3, 3, false>(p.w, a, stream);
         } else {
             a.b = static_cast<const uint16_t*>(hidden);
             a.b_plane = 0;
-            a.row_bits = bits;
+            a.row_bits = g.row_bits;
             st = launch_product<3, 1, false>(p.w, a, stream);
         }
         if (st != MOE_OK) return st;
         if (p.w.nsplit > 1)
             st = launch(sum_parts_kernel, grid_of(w_quads), dim3(256), 0, stream,
-                        reinterpret_cast<const float4*>(ws + p.parts), p.w.nsplit, w_quads, scale,
+                        reinterpret_cast<const float4*>(ws + p.parts), p.w.nsplit, w_quads,
                         reinterpret_cast<float4*>(d_W));
     }
     return st;
