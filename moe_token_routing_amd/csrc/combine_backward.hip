@@ -16,10 +16,13 @@
 // is summed in registers and only one row of partial sums per block is
 // written; a last kernel adds those in block order.
 //
-// Rows and slots need not match one to one. The slots of each row are counted
-// first (integer atomics); the main kernel writes the rows that one slot
-// names, and the row kernel the others: zeros for none, and for several the
-// sum over their slots in slot order.
+// Rows and slots need not match one to one. The main kernel writes every named
+// row's gradient and, for each row, a slot that names it (`owner`: any of them
+// stays). The row kernel then finds the rows to mend: an owner that does not
+// name its row is what the workspace held before, so no slot names the row and
+// it gets zeros (checking the owner against the slots saves clearing it); a slot
+// that is not the owner of its row says that several name it, and the row's
+// gradient is computed anew as the sum over them in slot order.
 #include <cmath>
 
 #include "launch.hpp"
@@ -31,83 +34,81 @@ namespace {
 constexpr int kSmallBlock = 256;
 constexpr int kWideBlock = 512;   // rows of more than 1024 vectors
 
-__global__ __launch_bounds__(kSmallBlock) void clear_kernel(int32_t* __restrict__ p, int n) {
-    for (long long i = blockIdx.x * static_cast<long long>(kSmallBlock) + threadIdx.x; i < n;
-         i += static_cast<long long>(gridDim.x) * kSmallBlock)
-        p[i] = 0;
-}
-
-__global__ __launch_bounds__(kSmallBlock) void count_rows_kernel(const int32_t* __restrict__ slots, int n, int R,
-                                                                 int32_t* __restrict__ named) {
-    for (long long f = blockIdx.x * static_cast<long long>(kSmallBlock) + threadIdx.x; f < n;
-         f += static_cast<long long>(gridDim.x) * kSmallBlock) {
-        const int r = slots[f];
-        if (r >= 0 && r < R) atomicAdd(&named[r], 1);
-    }
-}
-
 __device__ __forceinline__ float bf16_at(const u32x4& v, int e) {
     const uint32_t w = v[e >> 1];
     return e & 1 ? bf16_hi(w) : bf16_lo(w);
 }
 
-// TPT threads per token: 0 for tpt < 64 (a power of two, so a wave holds
-// several tokens), 64 (a token per wave), or BLOCK (a token per block). Thread
-// tid of a token owns vectors tid + i tpt of its rows, i < VPT.
 // Makes the compiler forget what it derived from a register, so that it unpacks
 // a row again where it is used next instead of keeping the unpacked values.
 __device__ __forceinline__ void keep_packed(u32x4& v) { asm volatile("" : "+v"(v)); }
 
-template <int VPT, int TPT, int BLOCK>
-__global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void combine_backward_kernel(
-    const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
-    const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
-    float gain_center, float eps, int T, int H, int k, int tpt, const int32_t* __restrict__ named,
-    u32x4* __restrict__ d_rows, float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
-    constexpr int G = VPT >= 3 ? 4 : 8;   // rows a group: up to 64 registers of row data
-    constexpr int kBlockWaves = BLOCK / kWave;
-    __shared__ float red[2][kBlockWaves][2 * G];
-    extern __shared__ float gain_lds[];
-    if (TPT != 0) tpt = TPT;
-    const int groups = BLOCK / tpt;   // tokens of a block
-    const int sub = TPT >= kWave ? __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / TPT)
-                                 : static_cast<int>(threadIdx.x) / tpt;
-    const int tid = static_cast<int>(threadIdx.x) - sub * tpt;
-    const int lane = __lane_id();
-    const int wave = threadIdx.x / kWave;
+// The block's row of partial gain gradients: its token groups' in order, each
+// group's vectors tid + i tpt.
+template <int VPT, int BLOCK>
+__device__ __forceinline__ void store_gain_part(const float (&dgain)[VPT][8], int sub, int tid, int tpt, int H,
+                                                float* lds, float* __restrict__ out) {
     const int nvec = H >> 3;
-    const float inv_h = 1.0f / static_cast<float>(H);
-
-    float gain[VPT][8], dgain[VPT][8];
+    if (tpt == BLOCK) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = tid + i * tpt;
+            if (v < nvec) {
+                float4* p = reinterpret_cast<float4*>(out) + 2 * v;
+                p[0] = make_float4(dgain[i][0], dgain[i][1], dgain[i][2], dgain[i][3]);
+                p[1] = make_float4(dgain[i][4], dgain[i][5], dgain[i][6], dgain[i][7]);
+            }
+        }
+        return;
+    }
 #pragma unroll
     for (int i = 0; i < VPT; ++i) {
         const int v = tid + i * tpt;
+        if (v < nvec)
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            gain[i][e] = v < nvec ? gain_center + norm_w[v * 8 + e] : 0.f;
-            dgain[i][e] = 0.f;
-        }
+            for (int e = 0; e < 8; ++e) lds[sub * H + v * 8 + e] = dgain[i][e];
     }
-    int buf = 0;
+    __syncthreads();
+    for (int c = threadIdx.x; c < H; c += BLOCK) {
+        float s = lds[c];
+        for (int q = 1; q < BLOCK / tpt; ++q) s += lds[q * H + c];
+        out[c] = s;
+    }
+}
+
+// Rows of up to 32 vectors: tpt threads per token (a power of two), one vector
+// each, several tokens in a wave.
+__global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
+    const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
+    const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
+    float gain_center, float eps, int T, int H, int k, int tpt, int32_t* __restrict__ owner,
+    u32x4* __restrict__ d_rows, float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
+    constexpr int G = 4;   // rows in flight
+    extern __shared__ float gain_lds[];
+    const int groups = kSmallBlock / tpt;   // tokens of a block
+    const int sub = static_cast<int>(threadIdx.x) / tpt;
+    const int tid = static_cast<int>(threadIdx.x) - sub * tpt;
+    const int nvec = H >> 3;
+    const bool mine = tid < nvec;
+    const float inv_h = 1.0f / static_cast<float>(H);
+    float gain[8], dgain[1][8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) {
+        gain[e] = mine ? gain_center + norm_w[tid * 8 + e] : 0.f;
+        dgain[0][e] = 0.f;
+    }
     const long long stride = static_cast<long long>(gridDim.x) * groups;
     for (long long t0 = static_cast<long long>(blockIdx.x) * groups; t0 < T; t0 += stride) {
         const long long t = t0 + sub;
         const bool tok_ok = t < T;
-        u32x4 y[VPT];
-        float acc[VPT][8];   // sum over the slots of w rstd x
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = tid + i * tpt;
-            y[i] = u32x4{0, 0, 0, 0};
-            if (tok_ok && v < nvec) y[i] = d_out[t * nvec + v];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) acc[i][e] = 0.f;
-        }
+        u32x4 y = {0, 0, 0, 0};
+        if (tok_ok && mine) y = d_out[t * nvec + tid];
+        float acc[8] = {};   // sum over the slots of w rstd x
         for (int j0 = 0; j0 < k; j0 += G) {
-            u32x4 x[G][VPT];
-            float wt[G], sums[2 * G];
+            u32x4 x[G];
+            float wt[G];
             int row[G];
-            bool ok[G], sole[G];
+            bool ok[G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
                 const int j = j0 + g;
@@ -118,41 +119,158 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
                     wt[g] = topk_w[t * k + j];
                 }
                 ok[g] = row[g] >= 0 && row[g] < R;
-                sole[g] = false;
-#pragma unroll
-                for (int i = 0; i < VPT; ++i) x[g][i] = u32x4{0, 0, 0, 0};
-                if (ok[g]) {
-                    sole[g] = named[row[g]] == 1;
-                    const u32x4* src = expert_out + static_cast<size_t>(row[g]) * nvec;
-#pragma unroll
-                    for (int i = 0; i < VPT; ++i) {
-                        const int v = tid + i * tpt;
-                        if (v < nvec) x[g][i] = load_nt(&src[v]);
-                    }
-                }
+                x[g] = u32x4{0, 0, 0, 0};
+                if (ok[g] && mine) x[g] = load_nt(&expert_out[static_cast<size_t>(row[g]) * nvec + tid]);
             }
 #pragma unroll
             for (int g = 0; g < G; ++g) {
+                const int j = j0 + g;
                 float ss = 0.f, a = 0.f;
-                if (ok[g]) {
 #pragma unroll
-                    for (int i = 0; i < VPT; ++i) {
+                for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][q], ss);
 #pragma unroll
-                        for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][i][q], ss);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e)
-                            a = __builtin_fmaf(bf16_at(x[g][i], e), bf16_at(y[i], e) * gain[i][e], a);
-                    }
+                for (int e = 0; e < 8; ++e) a = __builtin_fmaf(bf16_at(x[g], e), bf16_at(y, e) * gain[e], a);
+                ss = group_sum(ss, tpt);
+                a = group_sum(a, tpt);
+                if (tok_ok && j < k && tid == 0 && !ok[g]) d_topk_w[t * k + j] = 0.f;
+                if (!ok[g]) continue;
+                const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
+                const float ra = rstd * a;
+                if (tid == 0) {
+                    d_topk_w[t * k + j] = ra;
+                    owner[row[g]] = static_cast<int32_t>(t * k + j);
                 }
-                sums[2 * g] = ss;
-                sums[2 * g + 1] = a;
+                const float c = wt[g] * rstd;
+                const float d = rstd * (ra * inv_h);
+                float o[8];
+#pragma unroll
+                for (int e = 0; e < 8; ++e) {
+                    const float xe = bf16_at(x[g], e);
+                    acc[e] = __builtin_fmaf(c, xe, acc[e]);
+                    o[e] = c * __builtin_fmaf(-xe, d, bf16_at(y, e) * gain[e]);
+                }
+                if (mine)
+                    store_nt(u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
+                                   cvt_pk_bf16(o[6], o[7])},
+                             &d_rows[static_cast<size_t>(row[g]) * nvec + tid]);
             }
-            if constexpr (TPT == 0) {
+        }
 #pragma unroll
-                for (int i = 0; i < 2 * G; ++i) sums[i] = group_sum(sums[i], tpt);
+        for (int e = 0; e < 8; ++e) dgain[0][e] = __builtin_fmaf(bf16_at(y, e), acc[e], dgain[0][e]);
+    }
+    if (part_gain)
+        store_gain_part<1, kSmallBlock>(dgain, sub, tid, tpt, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
+}
+
+// A token per wave (TPT = 64) or per block (TPT = BLOCK). Thread tid of a token
+// owns vectors tid + i TPT of its rows, i < VPT. Lane j of every wave holds pick
+// j's slot and weight (k <= 32), loaded one token ahead; the rows of the next G
+// picks, the next token's first ones included, are in flight while the current
+// ones are summed and written.
+template <int VPT, int TPT, int BLOCK>
+__global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void combine_backward_kernel(
+    const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
+    const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
+    float gain_center, float eps, int T, int H, int k, int32_t* __restrict__ owner, u32x4* __restrict__ d_rows,
+    float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
+    constexpr int G = VPT <= 2 ? 4 : 2;   // rows a group: up to 32 registers of row data, and the next group's
+    // the sum over a token's slots of w rstd x, times y once per token; with
+    // four vectors a thread there are no registers for it, and each slot's
+    // product goes to the gain's gradient at once
+    constexpr bool SUM = VPT < 4;
+    constexpr int kBlockWaves = BLOCK / kWave;
+    __shared__ float red[2][kBlockWaves][2 * G];
+    extern __shared__ float gain_lds[];
+    constexpr int groups = BLOCK / TPT;   // tokens of a block
+    const int sub = __builtin_amdgcn_readfirstlane(static_cast<int>(threadIdx.x) / TPT);
+    const int tid = static_cast<int>(threadIdx.x) - sub * TPT;
+    const int lane = __lane_id();
+    const int wave = threadIdx.x / kWave;
+    const int nvec = H >> 3;
+    const float inv_h = 1.0f / static_cast<float>(H);
+
+    float gain[VPT][8], dgain[VPT][8];
+#pragma unroll
+    for (int i = 0; i < VPT; ++i) {
+        const int v = tid + i * TPT;
+#pragma unroll
+        for (int e = 0; e < 8; ++e) {
+            gain[i][e] = v < nvec ? gain_center + norm_w[v * 8 + e] : 0.f;
+            dgain[i][e] = 0.f;
+        }
+    }
+    auto load_picks = [&](long long t, int& r, float& w) {
+        r = -1;
+        w = 0.f;
+        if (t < T && lane < k) {
+            r = slots[t * k + lane];
+            w = topk_w[t * k + lane];
+            if (r >= R) r = -1;
+        }
+    };
+    auto load_token = [&](long long t, u32x4 (&y)[VPT]) {
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            const int v = tid + i * TPT;
+            y[i] = u32x4{0, 0, 0, 0};
+            if (t < T && v < nvec) y[i] = d_out[t * nvec + v];
+        }
+    };
+    // lanes k .. 63 hold slot -1, and j0 + G - 1 < 64
+    auto load_rows = [&](int r, int j0, u32x4 (&x)[G][VPT]) {
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int row = __builtin_amdgcn_readlane(r, j0 + g);
+#pragma unroll
+            for (int i = 0; i < VPT; ++i) x[g][i] = u32x4{0, 0, 0, 0};
+            if (row >= 0) {
+                const u32x4* src = expert_out + static_cast<size_t>(row) * nvec;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+                    const int v = tid + i * TPT;
+                    if (v < nvec) x[g][i] = load_nt(&src[v]);
+                }
+            }
+        }
+    };
+    const long long stride = static_cast<long long>(gridDim.x) * groups;
+    long long t = static_cast<long long>(blockIdx.x) * groups + sub;
+    int pick_r, next_r;
+    float pick_w, next_w;
+    u32x4 y[VPT], x[G][VPT];
+    load_picks(t, pick_r, pick_w);
+    load_token(t, y);
+    load_picks(t + stride, next_r, next_w);
+    load_rows(pick_r, 0, x);
+    int buf = 0;
+    // the tokens of a block's groups start together, so that with a token per
+    // block every thread takes the same turns
+    for (; t < T; t += stride) {
+        float acc[SUM ? VPT : 1][8] = {};
+        u32x4 yn[VPT];
+        float ra_of = 0.f;   // lane j: pick j's gradient
+        for (int j0 = 0; j0 < k; j0 += G) {
+            u32x4 xn[G][VPT];
+            if (j0 + G < k) {
+                load_rows(pick_r, j0 + G, xn);
             } else {
+                load_token(t + stride, yn);
+                load_rows(next_r, 0, xn);
+            }
+            float sums[2 * G];
 #pragma unroll
-                for (int i = 0; i < 2 * G; ++i) sums[i] = wave_sum(sums[i]);
+            for (int g = 0; g < G; ++g) {
+                float ss = 0.f, a = 0.f;
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][i][q], ss);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        a = __builtin_fmaf(bf16_at(x[g][i], e), bf16_at(y[i], e) * gain[i][e], a);
+                }
+                sums[2 * g] = wave_sum(ss);
+                sums[2 * g + 1] = wave_sum(a);
             }
             if constexpr (TPT == BLOCK) {
                 if (lane == 0) {
@@ -171,143 +289,170 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
             for (int i = 0; i < VPT; ++i) keep_packed(y[i]);
 #pragma unroll
             for (int g = 0; g < G; ++g) {
+                const int row = __builtin_amdgcn_readlane(pick_r, j0 + g);
+                if (row < 0) continue;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) keep_packed(x[g][i]);
-                const int j = j0 + g;
-                if (tok_ok && j < k && tid == 0 && !ok[g]) d_topk_w[t * k + j] = 0.f;
-                if (!ok[g]) continue;
+                const float w = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(pick_w), j0 + g));
                 const float rstd = 1.0f / sqrtf(sums[2 * g] * inv_h + eps);
                 const float ra = rstd * sums[2 * g + 1];
-                if (tid == 0) d_topk_w[t * k + j] = ra;
-                const float c = wt[g] * rstd;
+                if (lane == j0 + g) ra_of = ra;
+                const float c = w * rstd;
                 const float d = rstd * (ra * inv_h);
-                u32x4* dst = d_rows + static_cast<size_t>(row[g]) * nvec;
+                u32x4* dst = d_rows + static_cast<size_t>(row) * nvec;
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) {
-                    const int v = tid + i * tpt;
+                    const int v = tid + i * TPT;
                     float o[8];
 #pragma unroll
                     for (int e = 0; e < 8; ++e) {
                         const float xe = bf16_at(x[g][i], e);
-                        acc[i][e] = __builtin_fmaf(c, xe, acc[i][e]);
+                        if constexpr (SUM) acc[i][e] = __builtin_fmaf(c, xe, acc[i][e]);
+                        else dgain[i][e] = __builtin_fmaf(c * xe, bf16_at(y[i], e), dgain[i][e]);
                         o[e] = c * __builtin_fmaf(-xe, d, bf16_at(y[i], e) * gain[i][e]);
                     }
-                    if (sole[g] && v < nvec) {
-                        const u32x4 out = {cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]),
-                                           cvt_pk_bf16(o[4], o[5]), cvt_pk_bf16(o[6], o[7])};
-                        store_nt(out, &dst[v]);
-                    }
+                    if (v < nvec)
+                        store_nt(u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
+                                       cvt_pk_bf16(o[6], o[7])},
+                                 &dst[v]);
+                }
+            }
+#pragma unroll
+            for (int g = 0; g < G; ++g)
+#pragma unroll
+                for (int i = 0; i < VPT; ++i) x[g][i] = xn[g][i];
+        }
+        if (tid < k) {   // the token's first wave; k <= 32
+            d_topk_w[t * k + tid] = ra_of;
+            if (pick_r >= 0) owner[pick_r] = static_cast<int32_t>(t * k + tid);
+        }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) {
+            if constexpr (SUM) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e) dgain[i][e] = __builtin_fmaf(bf16_at(y[i], e), acc[i][e], dgain[i][e]);
+            }
+            y[i] = yn[i];
+        }
+        pick_r = next_r;
+        pick_w = next_w;
+        load_picks(t + 2 * stride, next_r, next_w);
+    }
+    if (part_gain)
+        store_gain_part<VPT, BLOCK>(dgain, sub, tid, TPT, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
+}
+
+// The gradient of row r as the sum over the slots that name it, in slot order,
+// by one wave. The slots are scanned for each 64 vectors of the row, twice: this
+// is for the odd row that several slots name, not for speed.
+__device__ __forceinline__ void repeated_row(const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out,
+                                             const int32_t* __restrict__ slots, const float* __restrict__ topk_w,
+                                             const float* __restrict__ norm_w, float gain_center, float eps, int n,
+                                             int H, int k, int r, u32x4* __restrict__ d_rows) {
+    const int lane = __lane_id();
+    const int nvec = H >> 3;
+    const u32x4* src = expert_out + static_cast<size_t>(r) * nvec;
+    u32x4* dst = d_rows + static_cast<size_t>(r) * nvec;
+    // sum over the row's slots of w y for vector v
+    auto gathered = [&](int v, float (&s)[8]) {
+#pragma unroll
+        for (int e = 0; e < 8; ++e) s[e] = 0.f;
+        for (int f0 = 0; f0 < n; f0 = n - f0 > kWave ? f0 + kWave : n) {
+            uint64_t hit = ballot(lane < n - f0 && slots[f0 + lane] == r);
+            while (hit) {
+                const int f = f0 + __builtin_ctzll(hit);
+                hit &= hit - 1;
+                const float w = topk_w[f];
+                if (v < nvec) {
+                    const u32x4 y = d_out[static_cast<size_t>(f / k) * nvec + v];
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(w, bf16_at(y, e), s[e]);
                 }
             }
         }
+    };
+    float ss = 0.f, a = 0.f;
+    for (int v0 = 0; v0 < nvec; v0 += kWave) {
+        const int v = v0 + lane;
+        float s[8];
+        gathered(v, s);
+        if (v < nvec) {
+            const u32x4 x = src[v];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i)
-#pragma unroll
-            for (int e = 0; e < 8; ++e) dgain[i][e] = __builtin_fmaf(bf16_at(y[i], e), acc[i][e], dgain[i][e]);
-    }
-    if (!part_gain) return;
-    // the block's row of partial gain gradients: its token groups in order
-    float* out = part_gain + static_cast<size_t>(blockIdx.x) * H;
-    if constexpr (TPT == BLOCK) {
-#pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = tid + i * tpt;
-            if (v < nvec) {
-                float4* p = reinterpret_cast<float4*>(out) + 2 * v;
-                p[0] = make_float4(dgain[i][0], dgain[i][1], dgain[i][2], dgain[i][3]);
-                p[1] = make_float4(dgain[i][4], dgain[i][5], dgain[i][6], dgain[i][7]);
+            for (int e = 0; e < 8; ++e) {
+                const float xe = bf16_at(x, e);
+                ss = __builtin_fmaf(xe, xe, ss);
+                a = __builtin_fmaf(xe, s[e] * (gain_center + norm_w[v * 8 + e]), a);
             }
         }
-    } else {
+    }
+    ss = wave_sum(ss);
+    a = wave_sum(a);
+    const float inv_h = 1.0f / static_cast<float>(H);
+    const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
+    const float d = rstd * (rstd * a * inv_h);
+    for (int v0 = 0; v0 < nvec; v0 += kWave) {
+        const int v = v0 + lane;
+        float s[8];
+        gathered(v, s);
+        if (v < nvec) {
+            const u32x4 x = src[v];
+            float o[8];
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            const int v = tid + i * tpt;
-            if (v < nvec)
-#pragma unroll
-                for (int e = 0; e < 8; ++e) gain_lds[sub * H + v * 8 + e] = dgain[i][e];
-        }
-        __syncthreads();
-        for (int c = threadIdx.x; c < H; c += BLOCK) {
-            float s = gain_lds[c];
-            for (int q = 1; q < groups; ++q) s += gain_lds[q * H + c];
-            out[c] = s;
+            for (int e = 0; e < 8; ++e)
+                o[e] = rstd * __builtin_fmaf(-bf16_at(x, e), d, s[e] * (gain_center + norm_w[v * 8 + e]));
+            dst[v] = u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
+                           cvt_pk_bf16(o[6], o[7])};
         }
     }
 }
 
-// One wave per row that no slot or several slots name.
+// Rows and slots [8 w, 8 w + 8) by wave w: zeros for rows without a slot, the
+// sum for rows with several. Eight, so that the unnamed rows at a dispatch's end
+// spread over many waves. The first of a row's slots that finds another one as
+// its owner claims the row by turning the owner into its complement; the
+// complement still says who the owner is.
+constexpr int kRowsPerWave = 8;
+
 __global__ __launch_bounds__(kSmallBlock) void combine_backward_rows_kernel(
     const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
     const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
-    float gain_center, float eps, int T, int H, int k, const int32_t* __restrict__ named,
-    u32x4* __restrict__ d_rows) {
+    float gain_center, float eps, int n, int H, int k, int32_t* owner, u32x4* __restrict__ d_rows) {
     const int lane = __lane_id();
     const int nvec = H >> 3;
-    const int waves = kSmallBlock / kWave;
-    const long long n = static_cast<long long>(T) * k;
-    for (long long r = static_cast<long long>(blockIdx.x) * waves + threadIdx.x / kWave; r < R;
-         r += static_cast<long long>(gridDim.x) * waves) {
-        const int count = __builtin_amdgcn_readfirstlane(named[r]);
-        if (count == 1) continue;
-        u32x4* dst = d_rows + r * nvec;
-        if (count == 0) {
+    const long long items = R > n ? R : n;
+    const long long stride = static_cast<long long>(gridDim.x) * (kSmallBlock / kWave) * kRowsPerWave;
+    for (long long i0 = (static_cast<long long>(blockIdx.x) * (kSmallBlock / kWave) + threadIdx.x / kWave) * kRowsPerWave;
+         i0 < items; i0 += stride) {
+        const long long i = i0 + lane;
+        bool unnamed = false, repeated = false;
+        int r = 0;
+        if (lane < kRowsPerWave && i < R) {
+            const int o = __hip_atomic_load(&owner[i], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+            const int f = o < 0 ? ~o : o;
+            unnamed = f >= n || slots[f] != i;
+        }
+        if (lane < kRowsPerWave && i < n) {
+            r = slots[i];
+            if (r >= 0 && r < R) {
+                int o = __hip_atomic_load(&owner[r], __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+                repeated = o >= 0 && o != i &&
+                           __hip_atomic_compare_exchange_strong(&owner[r], &o, ~o, __ATOMIC_RELAXED, __ATOMIC_RELAXED,
+                                                                __HIP_MEMORY_SCOPE_AGENT);
+            }
+        }
+        uint64_t todo = ballot(unnamed);
+        while (todo) {
+            const long long row = i0 + __builtin_ctzll(todo);
+            todo &= todo - 1;
+            u32x4* dst = d_rows + row * nvec;
             for (int v = lane; v < nvec; v += kWave) store_nt(u32x4{0, 0, 0, 0}, &dst[v]);
-            continue;
         }
-        const u32x4* src = expert_out + r * nvec;
-        // sum over the row's slots, in slot order, of w y for vector v
-        auto gathered = [&](int v, float (&s)[8]) {
-#pragma unroll
-            for (int e = 0; e < 8; ++e) s[e] = 0.f;
-            int left = count;
-            for (long long f0 = 0; f0 < n && left > 0; f0 += kWave) {
-                uint64_t hit = ballot(f0 + lane < n && slots[f0 + lane] == r);
-                while (hit) {
-                    const long long f = f0 + __builtin_ctzll(hit);
-                    hit &= hit - 1;
-                    --left;
-                    const float w = topk_w[f];
-                    if (v < nvec) {
-                        const u32x4 y = d_out[(f / k) * nvec + v];
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) s[e] = __builtin_fmaf(w, bf16_at(y, e), s[e]);
-                    }
-                }
-            }
-        };
-        float ss = 0.f, a = 0.f;
-        for (int v0 = 0; v0 < nvec; v0 += kWave) {
-            const int v = v0 + lane;
-            float s[8];
-            gathered(v, s);
-            if (v < nvec) {
-                const u32x4 x = src[v];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xe = bf16_at(x, e);
-                    ss = __builtin_fmaf(xe, xe, ss);
-                    a = __builtin_fmaf(xe, s[e] * (gain_center + norm_w[v * 8 + e]), a);
-                }
-            }
-        }
-        ss = wave_sum(ss);
-        a = wave_sum(a);
-        const float inv_h = 1.0f / static_cast<float>(H);
-        const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
-        const float d = rstd * (rstd * a * inv_h);
-        for (int v0 = 0; v0 < nvec; v0 += kWave) {
-            const int v = v0 + lane;
-            float s[8];
-            gathered(v, s);
-            if (v < nvec) {
-                const u32x4 x = src[v];
-                float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e)
-                    o[e] = rstd * __builtin_fmaf(-bf16_at(x, e), d, s[e] * (gain_center + norm_w[v * 8 + e]));
-                dst[v] = u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
-                               cvt_pk_bf16(o[6], o[7])};
-            }
+        todo = ballot(repeated);
+        while (todo) {
+            const int row = __builtin_amdgcn_readlane(r, __builtin_ctzll(todo));
+            todo &= todo - 1;
+            repeated_row(d_out, expert_out, slots, topk_w, norm_w, gain_center, eps, n, H, k, row, d_rows);
         }
     }
 }
@@ -336,7 +481,7 @@ __global__ __launch_bounds__(kGainCols* kGainGroups) void gain_reduce_kernel(con
 
 struct CombineBackwardPlan {
     int tpt, vpt, block, groups, grid;
-    size_t named, gain, bytes;
+    size_t owner, gain, bytes;
 };
 
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
@@ -361,7 +506,7 @@ inline CombineBackwardPlan plan_combine_backward(int T, int R, int H) {
     const int need = ceil_div(T, p.groups);
     const int most = 512;   // two blocks a CU
     p.grid = need < most ? need : most;
-    p.named = 0;
+    p.owner = 0;
     p.gain = round256(sizeof(int32_t) * static_cast<size_t>(R));
     p.bytes = p.gain + round256(sizeof(float) * static_cast<size_t>(p.grid) * H);
     if (p.bytes == 0) p.bytes = 256;
@@ -395,36 +540,21 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
         return MOE_ERR_ALIGN;
     const CombineBackwardPlan p = plan_combine_backward(T, R, H);
     if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
-    auto* named = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + p.named);
+    auto* owner = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + p.owner);
     auto* part = d_norm_w ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.gain) : nullptr;
     const auto* y = reinterpret_cast<const u32x4*>(d_out);
     const auto* x = reinterpret_cast<const u32x4*>(expert_out);
     auto* dx = reinterpret_cast<u32x4*>(d_expert_out);
-    const int most = 8 * device_cu_count();
-    auto grid_of = [&](long long n, int per) {
-        const long long g = (n + per - 1) / per;
-        return dim3(static_cast<unsigned>(g < most ? g : most));
-    };
     int st;
-    if (R > 0) {
-        st = launch(clear_kernel, grid_of(R, kSmallBlock), dim3(kSmallBlock), 0, stream, named, R);
-        if (st != MOE_OK) return st;
-        if (T > 0) {
-            st = launch(count_rows_kernel, grid_of(static_cast<long long>(T) * k, kSmallBlock), dim3(kSmallBlock), 0,
-                        stream, slots, T * k, R, named);
-            if (st != MOE_OK) return st;
-        }
-        st = launch(combine_backward_rows_kernel, grid_of(R, kSmallBlock / kWave), dim3(kSmallBlock), 0, stream, y,
-                    x, R, slots, topk_w, norm_w, gain_center, eps, T, H, k, named, dx);
-        if (st != MOE_OK) return st;
-    }
     if (T > 0) {
-#define MOE_CB_ARGS y, x, R, slots, topk_w, norm_w, gain_center, eps, T, H, k, p.tpt, named, dx, d_topk_w, part
+        const size_t lds = p.groups > 1 ? sizeof(float) * static_cast<size_t>(p.groups) * H : 0;
         auto run = [&](auto kern) {
-            const size_t lds = p.groups > 1 ? sizeof(float) * static_cast<size_t>(p.groups) * H : 0;
-            return launch(kern, dim3(p.grid), dim3(p.block), lds, stream, MOE_CB_ARGS);
+            return launch(kern, dim3(p.grid), dim3(p.block), lds, stream, y, x, R, slots, topk_w, norm_w, gain_center,
+                          eps, T, H, k, owner, dx, d_topk_w, part);
         };
-        if (p.tpt < kWave) st = run(combine_backward_kernel<1, 0, kSmallBlock>);
+        if (p.tpt < kWave)
+            st = launch(combine_backward_narrow_kernel, dim3(p.grid), dim3(p.block), lds, stream, y, x, R, slots,
+                        topk_w, norm_w, gain_center, eps, T, H, k, p.tpt, owner, dx, d_topk_w, part);
         else if (p.tpt == kWave)
             st = p.vpt == 1   ? run(combine_backward_kernel<1, kWave, kSmallBlock>)
                  : p.vpt == 2 ? run(combine_backward_kernel<2, kWave, kSmallBlock>)
@@ -437,7 +567,14 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
         else
             st = p.vpt <= 3 ? run(combine_backward_kernel<3, kWideBlock, kWideBlock>)
                             : run(combine_backward_kernel<4, kWideBlock, kWideBlock>);
-#undef MOE_CB_ARGS
+        if (st != MOE_OK) return st;
+    }
+    if (R > 0) {
+        const int n = T * k;
+        const long long blocks = ceil_div(R > n ? R : n, kRowsPerWave * (kSmallBlock / kWave));
+        const long long most = 16ll * device_cu_count();
+        st = launch(combine_backward_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
+                    dim3(kSmallBlock), 0, stream, y, x, R, slots, topk_w, norm_w, gain_center, eps, n, H, k, owner, dx);
         if (st != MOE_OK) return st;
     }
     if (!d_norm_w) return MOE_OK;
