@@ -84,7 +84,7 @@ enum moe_score {
  *   losses [2] FP32, counts [S,E] int32, probs [S,E] FP32, tokens [S+2] int32:
  *                outputs.
  *   workspace    at least moe_balance_loss_workspace_bytes(T, E, S) bytes
- *                (0: a size is out of range).
+ *                (0: a batch too small to need any, or a size out of range).
  * Errors: NULL_ARG, BAD_SHAPE, BAD_ARG (score), ALIGN, WORKSPACE, HIP.
  */
 size_t moe_balance_loss_workspace_bytes(int T, int E, int S);
@@ -134,7 +134,8 @@ int moe_balance_loss_backward(const float* d_losses, const float* logits, const 
  *   0 <= T <= MOE_MAX_TOKENS, 1 <= E <= MOE_MAX_EXPERTS, 1 <= K <= MOE_MAX_TOPK
  *   (K may exceed E).
  *   loss [1], token_loss [T] FP32, tokens [1] int32: outputs.
- *   workspace    at least moe_distill_loss_workspace_bytes(T, E) bytes.
+ *   workspace    at least moe_distill_loss_workspace_bytes(T, E) bytes (0: a
+ *                batch too small to need any, or a size out of range).
  * Errors: NULL_ARG, BAD_SHAPE, BAD_ARG (score, temperature), ALIGN, WORKSPACE,
  * HIP.
  */

@@ -3,19 +3,23 @@
 //
 // All four are passes over the [T,E] logits with little else to move, so they
 // are bound by reading the logits (and, backward, writing their gradient) once
-// each. One wave takes a token: its row stays in registers through the
-// maximum, the sums and the results (scores.hpp), and no pass reads it twice.
+// each, and in small batches by the chain of dependent steps. A token's row
+// stays in the registers of one wave (of a block's waves for wide rows,
+// scores.hpp) through the maximum, the sums and the results; a wave's first row
+// and picks are loaded before it knows whether its token is valid, so that
+// these loads and the mask's are one wait.
 //
-// Balance, forward: a block of four waves takes a chunk of tokens and, for
-// every sequence that crosses it, sums the probabilities per expert in its
-// lanes' registers (each lane owns fixed experts), counts the picks in LDS and
-// writes one row of partial sums. Row b + s holds block b's part of sequence
-// s: along the tokens either b or s grows, so no two parts share a row and
-// nothing needs clearing. A second kernel adds each sequence's rows in block
-// order and its last block, by a counter, forms the losses; only integers are
-// added atomically, so results do not depend on timing.
+// Balance, forward: a block takes a chunk of tokens and, for every sequence
+// that crosses it, sums the probabilities per expert in its lanes' registers
+// (each lane owns fixed experts), counts the picks in LDS and writes one row of
+// partial sums. Row b + s holds block b's part of sequence s: along the tokens
+// either b or s grows, so no two parts share a row and nothing needs clearing.
+// A second kernel adds each sequence's rows in block order and its last block,
+// by a counter, forms the losses; only integers are added atomically, so
+// results do not depend on timing. A batch of up to kSmallTokens tokens takes
+// one block of sixteen waves instead, which needs no second kernel and no
+// workspace: at such sizes a launch costs more than the work.
 #include <cmath>
-#include <type_traits>
 
 #include "launch.hpp"
 #include "scores.hpp"
@@ -23,15 +27,23 @@
 namespace moe {
 namespace {
 
-constexpr int kBlock = 256;
-constexpr int kWaves = kBlock / kWave;
 constexpr int kMaxChunk = 64;         // tokens of a block: one ballot holds their validity
-constexpr int kTargetBlocks = 1024;   // four blocks a CU
+constexpr int kGroups = 4;            // tokens of a block at a time where a wave takes a row
+constexpr int kTargetBlocks = 1024;   // four such blocks a CU
+constexpr int kFewTokens = 512;       // up to these a block takes one token of the balance loss: with many short
+                                      // sequences (15 tokens in 42) four tokens' sequences in turn took 18 us
+constexpr int kSmallGroups = 16;
+constexpr int kSmallTokens = 64;      // by one block, if their rows take one wave
+constexpr int kSmallExperts = 1024;
+constexpr int kBalanceOneWave = 1024, kDistillOneWave = 2560;   // widest rows that one wave takes
+constexpr int kSmallSequences = 4;    // taken in turn there
 
-// Tokens a block takes: as few as keep the grid within kTargetBlocks.
-inline int chunk_tokens(int T) {
-    int c = kWaves;
-    while (c < kMaxChunk && ceil_div(T, c) > kTargetBlocks) c *= 2;
+inline bool small_batch(int T, int E) { return T <= kSmallTokens && E <= kSmallExperts; }
+
+// Tokens a block takes: as few as keep the grid within `blocks`.
+inline int chunk_tokens(int T, bool one_wave, int blocks) {
+    int c = one_wave ? kGroups : 1;
+    while (c < kMaxChunk && ceil_div(T, c) > blocks) c *= 2;
     return c;
 }
 
@@ -41,111 +53,58 @@ __device__ __forceinline__ uint64_t valid_tokens(const uint8_t* __restrict__ mas
     return ballot(i < n && mask[t0 + i] != 0);
 }
 
-// ------------------------------------------------------------- balance ----
+// Bits [a, b) of a chunk's 64.
+__device__ __forceinline__ uint64_t bit_range(int a, int b) {
+    const uint64_t below_b = b >= 64 ? ~0ull : (1ull << b) - 1;
+    return below_b & ~((1ull << a) - 1);
+}
 
-template <int NV, bool SIGMOID>
-__global__ __launch_bounds__(kBlock) void balance_partial_kernel(
-    const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
-    const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, int chunk,
-    float* __restrict__ part_probs, int32_t* __restrict__ part_counts, int32_t* __restrict__ part_n,
-    float* __restrict__ part_z, int32_t* __restrict__ counter) {
-    extern __shared__ float lds[];
-    float* sum = lds;                                        // [E]
-    int32_t* hist = reinterpret_cast<int32_t*>(lds + E);     // [E]
-    __shared__ float zs[kWaves];
-    const int lane = __lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;   // for the kernel that follows
-    const int t0 = static_cast<int>(blockIdx.x) * chunk;
-    const int t1 = min(T, t0 + chunk);
-    const uint64_t valid = valid_tokens(mask, t0, t1 - t0);
+// The place of a wave in a block that takes GROUPS tokens at a time with WPT
+// waves each (one of the two is 1): its token group and its part of the row.
+template <int WPT, int GROUPS>
+struct Place {
+    static_assert(WPT == 1 || GROUPS == 1, "a token per wave, or the block's");
+    static constexpr int WAVES = WPT * GROUPS;
+    static constexpr int BLOCK = WAVES * kWave;
+    int lane, wave, group, part;
+    __device__ __forceinline__ Place() {
+        lane = __lane_id();
+        wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+        group = WPT == 1 ? wave : 0;
+        part = WPT == 1 ? 0 : wave;
+    }
+    // the bits of the chunk's tokens that fall to this wave's group
+    __device__ __forceinline__ uint64_t share() const {
+        return GROUPS == 1 ? ~0ull : (GROUPS == 4 ? 0x1111111111111111ull : 0x0001000100010001ull) << group;
+    }
+};
 
-    int a = t0;
-    while (a < t1) {
-        int begin = 0, end = 0;
-        const int s = find_sequence(seq_offsets, S, T, a, begin, end);
-        if (s < 0) {
-            // before the first sequence, or behind the last
-            const int first = seq_offset(seq_offsets, 0, T);
-            if (a >= first) break;
-            a = first;
-            continue;
-        }
-        const int b = min(end, t1);
-        for (int c = threadIdx.x; c < E; c += kBlock) hist[c] = 0;
-        __syncthreads();
-        for (int f = (a - t0) * k + static_cast<int>(threadIdx.x); f < (b - t0) * k; f += kBlock) {
-            if (valid >> (f / k) & 1) {
-                const int id = ids[static_cast<size_t>(t0) * k + f];
-                if (id >= 0 && id < E) atomicAdd(&hist[id], 1);
+// Calls body(t, row) for the tokens whose bits are set, in order, t relative to
+// the chunk. x holds row `have` already; the next token's row is loaded while
+// the current one is worked on, if two of them fit the registers.
+template <int NV, int WPT, typename F>
+__device__ __forceinline__ void for_rows(uint64_t bits, const float* __restrict__ logits, int E, int part, int lane,
+                                         Row<NV, WPT>& x, int have, F&& body) {
+    while (bits) {
+        const int t = __builtin_ctzll(bits);
+        bits &= bits - 1;
+        if (t != have) x.load(logits + static_cast<size_t>(t) * E, E, part, lane);
+        have = -1;
+        if constexpr (NV <= 4) {
+            Row<NV, WPT> row = x;
+            if (bits) {
+                have = __builtin_ctzll(bits);
+                x.load(logits + static_cast<size_t>(have) * E, E, part, lane);
             }
+            body(t, row);
+        } else {
+            body(t, x);
         }
-        float acc[NV][4];
-#pragma unroll
-        for (int i = 0; i < NV; ++i)
-#pragma unroll
-            for (int q = 0; q < 4; ++q) acc[i][q] = 0.f;
-        float z = 0.f;
-        for (int t = a + wave; t < b; t += kWaves) {
-            if (!(valid >> (t - t0) & 1)) continue;
-            float x[NV][4], u[NV][4];
-            load_row(logits + static_cast<size_t>(t) * E, E, lane, x);
-            float m = softmax_weights(x, u);
-            float total = row_sum(u);
-            const float lse = m + logf(total);
-            z += lse * lse;
-            if constexpr (SIGMOID) {
-                float none[1][4];
-                sigmoid_weights<NV, false>(x, u, none);
-                total = row_sum(u);
-            }
-            const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) acc[i][q] = __builtin_fmaf(u[i][q], inv, acc[i][q]);
-        }
-        if (lane == 0) zs[wave] = z;
-        // the four waves' sums, in wave order
-        for (int w = 0; w < kWaves; ++w) {
-            if (wave == w) {
-#pragma unroll
-                for (int i = 0; i < NV; ++i)
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        const int c = i * 256 + lane * 4 + q;
-                        if (c < E) sum[c] = w == 0 ? acc[i][q] : sum[c] + acc[i][q];
-                    }
-            }
-            __syncthreads();
-        }
-        const size_t row = static_cast<size_t>(blockIdx.x) + s;
-        for (int c = threadIdx.x; c < E; c += kBlock) {
-            part_probs[row * E + c] = sum[c];
-            part_counts[row * E + c] = hist[c];
-        }
-        if (threadIdx.x == 0) {
-            const uint64_t lo = valid >> (a - t0);
-            part_n[row] = __popcll(b - a < 64 ? lo & ((1ull << (b - a)) - 1) : lo);
-            float zt = zs[0];
-            for (int w = 1; w < kWaves; ++w) zt += zs[w];
-            part_z[row] = zt;
-        }
-        __syncthreads();
-        a = b;
     }
 }
 
-constexpr int kReduceBlock = 1024;
-constexpr int kReduceCols = 64;
-constexpr int kReduceGroups = kReduceBlock / kReduceCols;
-
-__device__ __forceinline__ float agent_load(const float* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
-__device__ __forceinline__ int32_t agent_load(const int32_t* p) {
-    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
-}
+// 1 / total, or 0 for a row whose every weight is zero.
+__device__ __forceinline__ float inverse(float total) { return total == 0.f ? 0.f : 1.f / total; }
 
 // Block sum of N doubles per thread, in a fixed order; thread 0 gets it.
 template <int N>
@@ -167,8 +126,194 @@ __device__ __forceinline__ void block_sum(double (&v)[N], double* red) {
     __syncthreads();
 }
 
-// Block s * col_blocks + c: columns [64 c, 64 c + 64) of sequence s, sixteen
-// groups of threads over its partial rows.
+// ------------------------------------------------------------- balance ----
+
+// Sums of one sequence's part of a block's tokens, [a, b) of the chunk at
+// `logits`: picks into hist[E] and, with a token per wave, each wave's
+// probabilities into sums[wave][E] (else they stay in acc, each wave's columns),
+// the token groups' sums of lse^2 into zs. Complete behind the last barrier.
+template <bool SIGMOID, int NV, int WPT, int GROUPS>
+__device__ __forceinline__ void balance_part(const Place<WPT, GROUPS>& at, const float* __restrict__ logits,
+                                             const int32_t* __restrict__ ids, uint64_t valid, int a, int b, int E,
+                                             int k, Row<NV, WPT>& first, int have, RowReduce<WPT>& reduce,
+                                             Row<NV, WPT>& acc, float* sums, int32_t* hist, float* zs) {
+    constexpr int BLOCK = Place<WPT, GROUPS>::BLOCK;
+    for (int c = threadIdx.x; c < E; c += BLOCK) hist[c] = 0;
+    __syncthreads();
+    for (int f = a * k + static_cast<int>(threadIdx.x); f < b * k; f += BLOCK) {
+        const int id = ids[f];
+        if ((valid >> (f / k) & 1) && id >= 0 && id < E) atomicAdd(&hist[id], 1);
+    }
+    acc.fill(0.f);
+    float z = 0.f;
+    for_rows(valid & bit_range(a, b) & at.share(), logits, E, at.part, at.lane, first, have,
+             [&](int, Row<NV, WPT>& x) {
+        Row<NV, WPT> u;
+        const float m = weight_origin(reduce.max(x.max()));
+        softmax_weights(x, m, u);
+        float total[2] = {u.sum(), 0.f};
+        if constexpr (SIGMOID) {
+            sigmoid_weights<false>(x, fminf(m, 0.f), u, u);
+            total[1] = u.sum();
+        }
+        reduce.sum(total);
+        const float lse = m + logf(total[0]);
+        z += lse * lse;
+        const float inv = inverse(total[SIGMOID ? 1 : 0]);
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) acc.v[i][q] = __builtin_fmaf(u.v[i][q], inv, acc.v[i][q]);
+    });
+    if (at.lane == 0 && at.part == 0) zs[at.group] = z;
+    if constexpr (WPT == 1) acc.store(sums + at.wave * E, E, 0, at.lane, false);
+    __syncthreads();
+}
+
+// Column c of the waves' sums, in wave order.
+template <int GROUPS>
+__device__ __forceinline__ float column_sum(const float* sums, int E, int c) {
+    float s = sums[c];
+#pragma unroll
+    for (int w = 1; w < GROUPS; ++w) s += sums[w * E + c];
+    return s;
+}
+
+template <int NV, int WPT, int GROUPS, bool SIGMOID>
+__global__ __launch_bounds__(WPT* GROUPS* kWave) void balance_partial_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, int chunk,
+    float* __restrict__ part_probs, int32_t* __restrict__ part_counts, int32_t* __restrict__ part_n,
+    float* __restrict__ part_z, int32_t* __restrict__ counter) {
+    using P = Place<WPT, GROUPS>;
+    extern __shared__ float lds[];
+    int32_t* hist = reinterpret_cast<int32_t*>(lds);   // [E]
+    float* sums = lds + E;                             // [GROUPS][E] with a token per wave
+    __shared__ float zs[GROUPS];
+    __shared__ float red[2][WPT][4];
+    const P at;
+    RowReduce<WPT> reduce{red, at.part};
+    if (blockIdx.x == 0 && threadIdx.x == 0) *counter = 0;   // for the kernel that follows
+    const int t0 = static_cast<int>(blockIdx.x) * chunk;
+    const int t1 = min(T, t0 + chunk);
+    Row<NV, WPT> first, acc;
+    int have = -1;
+    if (t0 + at.group < t1) {
+        have = at.group;
+        first.load(logits + static_cast<size_t>(t0 + at.group) * E, E, at.part, at.lane);
+    }
+    const uint64_t valid = valid_tokens(mask, t0, t1 - t0);
+    int a = t0;
+    while (a < t1) {
+        int begin = 0, end = 0;
+        const int s = find_sequence(seq_offsets, S, T, a, begin, end);
+        if (s < 0) {
+            // before the first sequence, or behind the last
+            const int start = seq_offset(seq_offsets, 0, T);
+            if (a >= start) break;
+            a = start;
+            continue;
+        }
+        const int b = min(end, t1);
+        balance_part<SIGMOID>(at, logits + static_cast<size_t>(t0) * E, ids + static_cast<size_t>(t0) * k, valid,
+                              a - t0, b - t0, E, k, first, have, reduce, acc, sums, hist, zs);
+        have = -1;
+        const size_t row = static_cast<size_t>(blockIdx.x) + s;
+        for (int c = threadIdx.x; c < E; c += P::BLOCK) {
+            part_counts[row * E + c] = hist[c];
+            if constexpr (WPT == 1) part_probs[row * E + c] = column_sum<GROUPS>(sums, E, c);
+        }
+        if constexpr (WPT > 1) acc.store(part_probs + row * E, E, at.part, at.lane, false);
+        if (threadIdx.x == 0) {
+            part_n[row] = __popcll(valid & bit_range(a - t0, b - t0));
+            float zt = zs[0];
+            for (int w = 1; w < GROUPS; ++w) zt += zs[w];
+            part_z[row] = zt;
+        }
+        __syncthreads();
+        a = b;
+    }
+}
+
+// A batch of up to kSmallTokens tokens, its sequences in turn.
+template <int NV, bool SIGMOID>
+__global__ __launch_bounds__(kSmallGroups* kWave) void balance_small_kernel(
+    const float* __restrict__ logits, const int32_t* __restrict__ ids, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ seq_offsets, int T, int E, int k, int S, float* __restrict__ losses,
+    int32_t* __restrict__ counts, float* __restrict__ probs, int32_t* __restrict__ tokens) {
+    using P = Place<1, kSmallGroups>;
+    static_assert(P::BLOCK >= kSmallExperts, "a thread per expert");
+    extern __shared__ float sums[];   // [kSmallGroups][E]
+    __shared__ int32_t hist[kSmallExperts];
+    __shared__ float zs[kSmallGroups];
+    __shared__ double red[kSmallGroups];
+    const P at;
+    RowReduce<1> reduce{nullptr, 0};
+    Row<NV, 1> first, acc;
+    int have = -1;
+    if (at.group < T) {
+        have = at.group;
+        first.load(logits + static_cast<size_t>(at.group) * E, E, 0, at.lane);
+    }
+    const uint64_t valid = valid_tokens(mask, 0, T);
+    const int c = threadIdx.x;
+    double balance = 0, z = 0;   // thread 0's
+    int n = 0, full = 0;
+    for (int s = 0; s < S; ++s) {
+        const int a = seq_offset(seq_offsets, s, T), b = seq_offset(seq_offsets, s + 1, T);
+        const int m = a < b ? __popcll(valid & bit_range(a, b)) : 0;
+        if (c == 0) tokens[s] = m;
+        float p = 0.f;
+        int32_t h = 0;
+        if (m > 0) {
+            balance_part<SIGMOID>(at, logits, ids, valid, a, b, E, k, first, have, reduce, acc, sums, hist, zs);
+            have = -1;
+            if (c < E) {
+                p = column_sum<kSmallGroups>(sums, E, c);
+                h = hist[c];
+            }
+            double v[1] = {static_cast<double>(p * static_cast<float>(h))};
+            block_sum(v, red);
+            if (c == 0) {
+                balance += v[0] * E / (static_cast<double>(k) * m * m);
+                for (int w = 0; w < kSmallGroups; ++w) z += zs[w];
+            }
+            n += m;
+            ++full;
+            __syncthreads();
+        }
+        if (c < E) {
+            probs[static_cast<size_t>(s) * E + c] = p;
+            counts[static_cast<size_t>(s) * E + c] = h;
+        }
+    }
+    if (c == 0) {
+        losses[0] = full > 0 ? static_cast<float>(balance / full) : 0.f;
+        losses[1] = n > 0 ? static_cast<float>(z / n) : 0.f;
+        tokens[S] = n;
+        tokens[S + 1] = full;
+    }
+}
+
+constexpr int kReduceBlock = 1024;
+
+template <typename V>
+__device__ __forceinline__ V agent_load(const V* p) {
+    return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+// Publishes a value to the whole device: written through to where agent_load
+// reads, and waited for (wait_stores). A __threadfence per block would write
+// back its XCD's L2 instead (the reduction 26 -> 10 us with 52 blocks).
+template <typename V>
+__device__ __forceinline__ void agent_store(V* p, V v) {
+    __hip_atomic_store(p, v, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ void wait_stores() { __builtin_amdgcn_s_waitcnt(0); }
+
+// Block s * col_blocks + c: columns [COLS c, COLS c + COLS) of sequence s,
+// 1024 / COLS groups of threads over its partial rows. Few columns spread one
+// sequence's sums over many CUs, many keep the blocks of many sequences few.
+template <int COLS>
 __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
     const float* __restrict__ part_probs, const int32_t* __restrict__ part_counts,
     const int32_t* __restrict__ part_n, const float* __restrict__ part_z,
@@ -176,20 +321,21 @@ __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
     float* __restrict__ losses, int32_t* __restrict__ counts, float* __restrict__ probs,
     int32_t* __restrict__ tokens, float* __restrict__ seq_dot, float* __restrict__ seq_z,
     int32_t* __restrict__ counter) {
-    __shared__ float sp[kReduceGroups][kReduceCols];
-    __shared__ int32_t sc[kReduceGroups][kReduceCols];
+    constexpr int kReduceGroups = kReduceBlock / COLS;
+    __shared__ float sp[kReduceGroups][COLS];
+    __shared__ int32_t sc[kReduceGroups][COLS];
     __shared__ double red[(kReduceBlock / kWave) * 4];
     __shared__ int last;
     const int s = blockIdx.x / col_blocks;
     const int cb = blockIdx.x - s * col_blocks;
-    const int col = threadIdx.x % kReduceCols, group = threadIdx.x / kReduceCols;
-    const int c = cb * kReduceCols + col;
+    const int col = threadIdx.x % COLS, group = threadIdx.x / COLS;
+    const int c = cb * COLS + col;
     const int a = seq_offset(seq_offsets, s, T), b = seq_offset(seq_offsets, s + 1, T);
     const int b0 = a / chunk, b1 = a < b ? (b - 1) / chunk + 1 : b0;
     float p = 0.f;
     int32_t n = 0;
     if (c < E) {
-#pragma unroll 4
+#pragma unroll 8
         for (int r = b0 + group; r < b1; r += kReduceGroups) {
             const size_t at = (static_cast<size_t>(r) + s) * E + c;
             p += part_probs[at];
@@ -198,49 +344,68 @@ __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
     }
     sp[group][col] = p;
     sc[group][col] = n;
-    __syncthreads();
-    if (group == 0) {
-        for (int g = 1; g < kReduceGroups; ++g) {
-            p += sp[g][col];
-            n += sc[g][col];
-        }
-        if (c < E) {
-            probs[static_cast<size_t>(s) * E + c] = p;
-            counts[static_cast<size_t>(s) * E + c] = n;
-        }
-        const float dot = wave_sum(p * static_cast<float>(n));   // the 64 columns are one wave
-        if (col == 0) seq_dot[static_cast<size_t>(s) * col_blocks + cb] = dot;
-    } else if (group == 1 && cb == 0) {
+    if (threadIdx.x >= kReduceBlock - kWave && cb == 0) {
         int32_t m = 0;
         float z = 0.f;
-        for (int r = b0 + col; r < b1; r += kReduceCols) {
+        const int i = threadIdx.x - (kReduceBlock - kWave);
+#pragma unroll 8
+        for (int r = b0 + i; r < b1; r += kWave) {
             m += part_n[r + s];
             z += part_z[r + s];
         }
         z = wave_sum(z);
         for (int off = 32; off >= 1; off >>= 1) m += __shfl_xor(m, off, kWave);
-        if (col == 0) {
-            tokens[s] = m;
-            seq_z[s] = z;
+        if (i == 0) {
+            agent_store(&tokens[s], m);
+            agent_store(&seq_z[s], z);
         }
     }
-    // the last block to get here has every sequence's sums before it
-    __threadfence();
     __syncthreads();
-    if (threadIdx.x == 0) last = atomicAdd(counter, 1) == S * col_blocks - 1;
+    // sixteen lanes a column add its groups, four columns a wave at a time
+    const int l16 = threadIdx.x % 16;
+    for (int q = threadIdx.x / 16; q < COLS; q += kReduceBlock / 16) {
+        p = 0.f;
+        n = 0;
+        for (int g = l16; g < kReduceGroups; g += 16) {
+            p += sp[g][q];
+            n += sc[g][q];
+        }
+        p = group_sum(p, 16);
+        for (int off = 8; off >= 1; off >>= 1) n += __shfl_xor(n, off, kWave);
+        if (l16 == 0) {
+            const int e = cb * COLS + q;
+            if (e < E) {
+                probs[static_cast<size_t>(s) * E + e] = p;
+                counts[static_cast<size_t>(s) * E + e] = n;
+            }
+            sp[0][q] = p * static_cast<float>(n);   // this column's first group: read above by these lanes alone
+        }
+    }
+    __syncthreads();
+    if (threadIdx.x < kWave) {
+        float dot = 0.f;
+        for (int q = threadIdx.x; q < COLS; q += kWave) dot += sp[0][q];
+        dot = wave_sum(dot);
+        if (threadIdx.x == 0) agent_store(&seq_dot[static_cast<size_t>(s) * col_blocks + cb], dot);
+    }
+    // the last block to count itself finds every block's values published
+    wait_stores();
+    __syncthreads();
+    if (threadIdx.x == 0)
+        last = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) == S * col_blocks - 1;
     __syncthreads();
     if (!last) return;
-    __threadfence();
     double v[4] = {0, 0, 0, 0};   // balance, z, tokens, sequences with a token
+    for (int i = threadIdx.x; i < S * col_blocks; i += kReduceBlock) {
+        const float dot = agent_load(&seq_dot[i]);
+        const double m = agent_load(&tokens[i / col_blocks]);
+        if (m > 0) v[0] += dot * static_cast<double>(E) / (k * m * m);
+    }
     for (int q = threadIdx.x; q < S; q += kReduceBlock) {
         const int32_t m = agent_load(&tokens[q]);
-        if (m == 0) continue;
-        double dot = 0;
-        for (int i = 0; i < col_blocks; ++i) dot += agent_load(&seq_dot[static_cast<size_t>(q) * col_blocks + i]);
-        v[0] += dot * E / (static_cast<double>(k) * m * m);
         v[1] += agent_load(&seq_z[q]);
         v[2] += m;
-        v[3] += 1;
+        v[3] += m > 0;
     }
     block_sum(v, red);
     if (threadIdx.x == 0) {
@@ -251,28 +416,35 @@ __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
     }
 }
 
-// Each wave takes the chunk's tokens in turn; the coefficients c_e of the
-// current sequence stay in its registers.
-template <int NV, bool SIGMOID>
-__global__ __launch_bounds__(kBlock) void balance_backward_kernel(
+// The chunk's tokens in turn; the coefficients c_e of the current sequence stay
+// in registers.
+template <int NV, int WPT, bool SIGMOID>
+__global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void balance_backward_kernel(
     const float* __restrict__ d_losses, const float* __restrict__ logits, const uint8_t* __restrict__ mask,
     const int32_t* __restrict__ seq_offsets, const int32_t* __restrict__ counts,
     const int32_t* __restrict__ tokens, int T, int E, int k, int S, int chunk, int accumulate,
     float* __restrict__ d_logits) {
-    const int lane = __lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    using P = Place<WPT, WPT == 1 ? kGroups : 1>;
+    __shared__ float red[2][WPT][4];
+    const P at;
+    RowReduce<WPT> reduce{red, at.part};
     const int t0 = static_cast<int>(blockIdx.x) * chunk;
-    const int t1 = min(T, t0 + chunk);
-    const uint64_t valid = valid_tokens(mask, t0, t1 - t0);
+    const int len = min(chunk, T - t0);
+    const float* rows = logits + static_cast<size_t>(t0) * E;
+    float* out = d_logits + static_cast<size_t>(t0) * E;
+    Row<NV, WPT> first;
+    if (at.group < len) first.load(rows + static_cast<size_t>(at.group) * E, E, at.part, at.lane);
+    const uint64_t valid = valid_tokens(mask, t0, len);
+    const uint64_t share = at.share() & bit_range(0, len);
     const float n = static_cast<float>(max(tokens[S], 1));
     const float full = static_cast<float>(max(tokens[S + 1], 1));
     const float zg = 2.f * d_losses[1] / n;
     int s = -1, begin = 0, end = 0;
-    float cf[NV][4] = {};
-    for (int t = t0 + wave; t < t1; t += kWaves) {
-        bool ok = valid >> (t - t0) & 1;
-        if (ok && !(s >= 0 && t < end)) {
-            s = find_sequence(seq_offsets, S, T, t, begin, end);
+    Row<NV, WPT> cf;
+    cf.fill(0.f);
+    for_rows(valid & share, rows, E, at.part, at.lane, first, at.group, [&](int t, Row<NV, WPT>& x) {
+        if (!(s >= 0 && t0 + t < end)) {
+            s = find_sequence(seq_offsets, S, T, t0 + t, begin, end);
             if (s >= 0) {
                 const float m = static_cast<float>(max(tokens[s], 1));
                 const float w = d_losses[0] * static_cast<float>(E) / (static_cast<float>(k) * m * m * full);
@@ -280,68 +452,55 @@ __global__ __launch_bounds__(kBlock) void balance_backward_kernel(
                 for (int i = 0; i < NV; ++i)
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int c = i * 256 + lane * 4 + q;
-                        cf[i][q] = c < E ? w * static_cast<float>(counts[static_cast<size_t>(s) * E + c]) : 0.f;
+                        const int c = cf.column(i, at.part, at.lane) + q;
+                        cf.v[i][q] = c < E ? w * static_cast<float>(counts[static_cast<size_t>(s) * E + c]) : 0.f;
                     }
             }
         }
-        ok = ok && s >= 0;
-        float* out = d_logits + static_cast<size_t>(t) * E;
-        float d[NV][4];
-        if (!ok) {
-            if (accumulate) continue;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[i][q] = 0.f;
-            store_row(out, E, lane, d, false);
-            continue;
+        Row<NV, WPT> d;
+        if (s < 0) {   // in no sequence: as invalid
+            d.fill(0.f);
+            if (!accumulate) d.store(out + static_cast<size_t>(t) * E, E, at.part, at.lane, false);
+            return;
         }
-        float x[NV][4], u[NV][4];
-        load_row(logits + static_cast<size_t>(t) * E, E, lane, x);
-        // the z loss' part: (2 / n) lse softmax
-        const float m = softmax_weights(x, u);
-        float total = row_sum(u);
-        const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
-        const float zc = zg == 0.f ? 0.f : zg * (m + logf(total)) * inv;
+        Row<NV, WPT> u;
+        const float m = weight_origin(reduce.max(x.max()));
+        softmax_weights(x, m, u);
         if constexpr (SIGMOID) {
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[i][q] = zc * u[i][q];
-            float slope[NV][4];
-            sigmoid_weights<NV, true>(x, u, slope);
-            total = row_sum(u);
-            const float pinv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
-            float dot = 0.f;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) dot = __builtin_fmaf(u[i][q], cf[i][q], dot);
-            dot = wave_sum(dot) * pinv;
+            d = u;
+            Row<NV, WPT> slope;
+            sigmoid_weights<true>(x, fminf(m, 0.f), u, slope);
+            float v[3] = {d.sum(), u.sum(), u.dot(cf)};
+            reduce.sum(v);
+            // the z loss' part: (2 / n) lse softmax
+            const float zc = zg == 0.f ? 0.f : zg * (m + logf(v[0])) * inverse(v[0]);
+            const float inv = inverse(v[1]), dot = v[2] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
                 for (int q = 0; q < 4; ++q)
-                    d[i][q] = __builtin_fmaf(u[i][q] * pinv * slope[i][q], cf[i][q] - dot, d[i][q]);
+                    d.v[i][q] = __builtin_fmaf(u.v[i][q] * inv * slope.v[i][q], cf.v[i][q] - dot, zc * d.v[i][q]);
         } else {
-            float dot = 0.f;
+            float v[2] = {u.sum(), u.dot(cf)};
+            reduce.sum(v);
+            const float inv = inverse(v[0]), dot = v[1] * inv;
+            const float zc = zg == 0.f ? 0.f : zg * (m + logf(v[0])) * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
-                for (int q = 0; q < 4; ++q) dot = __builtin_fmaf(u[i][q], cf[i][q], dot);
-            dot = wave_sum(dot) * inv;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) d[i][q] = u[i][q] * __builtin_fmaf(cf[i][q] - dot, inv, zc);
+                for (int q = 0; q < 4; ++q) d.v[i][q] = u.v[i][q] * __builtin_fmaf(cf.v[i][q] - dot, inv, zc);
         }
-        store_row(out, E, lane, d, accumulate);
-    }
+        d.store(out + static_cast<size_t>(t) * E, E, at.part, at.lane, accumulate);
+    });
+    if (accumulate) return;
+    Row<NV, WPT> zero;
+    zero.fill(0.f);
+    for (uint64_t bits = ~valid & share; bits; bits &= bits - 1)
+        zero.store(out + static_cast<size_t>(__builtin_ctzll(bits)) * E, E, at.part, at.lane, false);
 }
 
 struct BalancePlan {
-    int chunk, blocks, col_blocks;
+    int chunk, blocks, cols, col_blocks;
     size_t rows, probs, counts, n, z, dot, seq_z, counter, bytes;   // byte offsets
 };
 
@@ -351,11 +510,15 @@ inline bool balance_shape_ok(int T, int E, int S) {
     return T >= 0 && T <= MOE_MAX_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS && S >= 1 && S <= MOE_MAX_SEQUENCES;
 }
 
+inline bool balance_small(int T, int E, int S) { return small_batch(T, E) && S <= kSmallSequences; }
+
 inline BalancePlan plan_balance(int T, int E, int S) {
     BalancePlan p;
-    p.chunk = chunk_tokens(T);
+    p.chunk = T <= kFewTokens ? 1 : chunk_tokens(T, E <= kBalanceOneWave, kTargetBlocks);
     p.blocks = ceil_div(T, p.chunk);
-    p.col_blocks = ceil_div(E, kReduceCols);
+    p.cols = 16;
+    while (p.cols < 256 && static_cast<long long>(S) * ceil_div(E, p.cols) > 1024) p.cols *= 4;
+    p.col_blocks = ceil_div(E, p.cols);
     p.rows = static_cast<size_t>(p.blocks) + S;
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -376,99 +539,121 @@ inline BalancePlan plan_balance(int T, int E, int S) {
 
 // ------------------------------------------------------------- distill ----
 
-// Lane j < K: teacher entry j of token t, its share q of the entries' sum and
-// log q; id -1 where there is none. Returns whether the token has an entry.
-__device__ __forceinline__ bool teacher_shares(const int32_t* __restrict__ ids, const float* __restrict__ logits,
-                                               size_t t, int K, int E, int score, float inv_temp, int& id,
-                                               float& q, float& logq) {
-    const int lane = __lane_id();
-    id = -1;
+constexpr int kDistillBlocks = 2 * kTargetBlocks;   // no partial rows to add up: a token per wave sooner
+
+// Lane j < K: teacher entry j of token t; id -1 where there is none.
+struct Entry {
+    int id = -1;
     float z = kNegInf;
+};
+
+__device__ __forceinline__ Entry teacher_entry(const int32_t* __restrict__ ids, const float* __restrict__ logits,
+                                               size_t t, int K) {
+    Entry e;
+    const int lane = __lane_id();
     if (lane < K) {
-        id = ids[t * K + lane];
-        z = logits[t * K + lane];
-        if (id < 0 || id >= E || z == kNegInf) id = -1;
-        z = id < 0 ? kNegInf : log_score(z * inv_temp, score);
+        e.id = ids[t * K + lane];
+        e.z = logits[t * K + lane];
     }
+    return e;
+}
+
+// The entry's share q of the entries' sum and log q; id -1 where there is none.
+// Returns whether the token has an entry.
+__device__ __forceinline__ bool teacher_shares(const Entry& e, int E, int score, float inv_temp, int& id, float& q,
+                                               float& logq) {
+    id = e.id < 0 || e.id >= E || e.z == kNegInf ? -1 : e.id;
     if (ballot(id >= 0) == 0) return false;
+    const float z = id < 0 ? kNegInf : log_score(e.z * inv_temp, score);
     const float m = wave_max(z);
-    const float e = id < 0 ? 0.f : expf(z - m);
-    const float total = wave_sum(e);
+    const float w = id < 0 ? 0.f : expf(z - m);
+    const float total = wave_sum(w);
     logq = id < 0 ? 0.f : (z - m) - logf(total);
-    q = e / total;
+    q = w / total;
     return true;
 }
 
-template <int NV>
-__device__ __forceinline__ void scale_row(float (&x)[NV][4], float f) {
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) x[i][q] *= f;
-}
-
-template <int NV, bool SIGMOID>
-__global__ __launch_bounds__(kBlock) void distill_kernel(
+// GROUPS = kSmallGroups: one block for a batch of up to kSmallTokens tokens,
+// which writes the loss itself; else one partial sum per block.
+template <int NV, int WPT, int GROUPS, bool SIGMOID>
+__global__ __launch_bounds__(WPT* GROUPS* kWave) void distill_kernel(
     const float* __restrict__ logits, const int32_t* __restrict__ t_ids, const float* __restrict__ t_logits,
     const uint8_t* __restrict__ mask, float inv_temp, float temp2, int T, int E, int K, int chunk,
     float* __restrict__ token_loss, float* __restrict__ part_loss, int32_t* __restrict__ part_n) {
-    __shared__ float sl[kWaves];
-    __shared__ int32_t sn[kWaves];
+    __shared__ float sl[GROUPS];
+    __shared__ int32_t sn[GROUPS];
+    __shared__ float red[2][WPT][4];
     constexpr int score = SIGMOID ? MOE_SCORE_SIGMOID : MOE_SCORE_SOFTMAX;
-    const int lane = __lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+    const Place<WPT, GROUPS> at;
+    RowReduce<WPT> reduce{red, at.part};
     const int t0 = static_cast<int>(blockIdx.x) * chunk;
-    const int t1 = min(T, t0 + chunk);
-    const uint64_t valid = valid_tokens(mask, t0, t1 - t0);
+    const int len = min(chunk, T - t0);
+    const float* rows = logits + static_cast<size_t>(t0) * E;
+    Row<NV, WPT> first;
+    Entry entry;
+    if (at.group < len) {
+        first.load(rows + static_cast<size_t>(at.group) * E, E, at.part, at.lane);
+        entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + at.group, K);
+    }
+    const uint64_t valid = valid_tokens(mask, t0, len);
+    const uint64_t share = at.share() & bit_range(0, len);
+    const bool writes = at.lane == 0 && at.part == 0;
     float sum = 0.f;
     int32_t n = 0;
-    for (int t = t0 + wave; t < t1; t += kWaves) {
+    for_rows(valid & share, rows, E, at.part, at.lane, first, at.group, [&](int t, Row<NV, WPT>& x) {
+        const size_t tok = static_cast<size_t>(t0) + t;
+        if (t != at.group) entry = teacher_entry(t_ids, t_logits, tok, K);
+        float xp = 0.f;   // the student's logit of the entry
+        if (entry.id >= 0 && entry.id < E) xp = logits[tok * E + entry.id] * inv_temp;
         int id = -1;
         float q = 0.f, logq = 0.f, loss = 0.f;
-        if ((valid >> (t - t0) & 1) &&
-            teacher_shares(t_ids, t_logits, t, K, E, score, inv_temp, id, q, logq)) {
-            const float* row = logits + static_cast<size_t>(t) * E;
-            float x[NV][4], u[NV][4];
-            load_row(row, E, lane, x);
-            const float xp = id >= 0 ? row[id] * inv_temp : 0.f;
-            scale_row(x, inv_temp);
-            float m;
+        if (teacher_shares(entry, E, score, inv_temp, id, q, logq)) {
+            Row<NV, WPT> u;
+            x.scale(inv_temp);
+            float m = weight_origin(reduce.max(x.max()));
             if constexpr (SIGMOID) {
-                float none[1][4];
-                m = sigmoid_weights<NV, false>(x, u, none);
+                m = fminf(m, 0.f);
+                sigmoid_weights<false>(x, m, u, u);
             } else {
-                m = softmax_weights(x, u);
+                softmax_weights(x, m, u);
             }
-            const float lse = m + logf(row_sum(u));
+            float total[1] = {u.sum()};
+            reduce.sum(total);
+            const float lse = m + logf(total[0]);
             const float term = id >= 0 && q > 0.f ? q * (logq - (log_score(xp, score) - lse)) : 0.f;
             loss = temp2 * wave_sum(term);
             sum += loss;
             ++n;
         }
-        if (lane == 0) token_loss[t] = loss;
-    }
-    if (lane == 0) {
-        sl[wave] = sum;
-        sn[wave] = n;
+        if (writes) token_loss[tok] = loss;
+    });
+    for (uint64_t bits = ~valid & share; bits; bits &= bits - 1)
+        if (writes) token_loss[static_cast<size_t>(t0) + __builtin_ctzll(bits)] = 0.f;
+    if (writes) {
+        sl[at.group] = sum;
+        sn[at.group] = n;
     }
     __syncthreads();
     if (threadIdx.x == 0) {
-        for (int w = 1; w < kWaves; ++w) {
+        for (int w = 1; w < GROUPS; ++w) {
             sum += sl[w];
             n += sn[w];
         }
-        part_loss[blockIdx.x] = sum;
+        part_loss[blockIdx.x] = GROUPS != kSmallGroups ? sum : n > 0 ? sum / static_cast<float>(n) : 0.f;
         part_n[blockIdx.x] = n;
     }
 }
 
-__global__ __launch_bounds__(kBlock) void distill_reduce_kernel(const float* __restrict__ part_loss,
-                                                                const int32_t* __restrict__ part_n, int blocks,
-                                                                float* __restrict__ loss,
-                                                                int32_t* __restrict__ tokens) {
-    __shared__ double red[kWaves * 2];
+constexpr int kDistillReduceBlock = 256;
+
+__global__ __launch_bounds__(kDistillReduceBlock) void distill_reduce_kernel(const float* __restrict__ part_loss,
+                                                                             const int32_t* __restrict__ part_n,
+                                                                             int blocks, float* __restrict__ loss,
+                                                                             int32_t* __restrict__ tokens) {
+    __shared__ double red[kDistillReduceBlock / kWave * 2];
     double v[2] = {0, 0};
-    for (int b = threadIdx.x; b < blocks; b += kBlock) {
+#pragma unroll 4
+    for (int b = threadIdx.x; b < blocks; b += kDistillReduceBlock) {
         v[0] += part_loss[b];
         v[1] += part_n[b];
     }
@@ -481,40 +666,47 @@ __global__ __launch_bounds__(kBlock) void distill_reduce_kernel(const float* __r
 
 // The teacher's shares reach the lanes that own their experts through a row of
 // LDS per wave: zeros but for the entries, which are cleared again behind each
-// token. LDS operations of one wave run in order, so no barrier is needed.
-template <int NV, bool SIGMOID>
-__global__ __launch_bounds__(kBlock) void distill_backward_kernel(
+// token. Each wave keeps its own columns; LDS
+// operations of one wave run in order, so no barrier is needed.
+template <int NV, int WPT, bool SIGMOID>
+__global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void distill_backward_kernel(
     const float* __restrict__ d_loss, const float* __restrict__ logits, const int32_t* __restrict__ t_ids,
     const float* __restrict__ t_logits, const uint8_t* __restrict__ mask, const int32_t* __restrict__ tokens,
     float inv_temp, float temp, int T, int E, int K, int chunk, int accumulate, float* __restrict__ d_logits) {
     extern __shared__ float lds[];
+    __shared__ float red[2][WPT][4];
     constexpr int score = SIGMOID ? MOE_SCORE_SIGMOID : MOE_SCORE_SOFTMAX;
-    const int lane = __lane_id();
-    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-    float* share = lds + wave * (NV * 256);
+    const Place<WPT, WPT == 1 ? kGroups : 1> at;
+    RowReduce<WPT> reduce{red, at.part};
+    // a wave's columns, 256 at a time: column c of the row is at
+    // 256 (c / (256 WPT)) + c % 256 of the wave c / 256 % WPT that owns it
+    float* shares = lds + at.wave * (NV * 256);
+    auto place = [&](int c) { return (c / (256 * WPT)) * 256 + c % 256; };
 #pragma unroll
-    for (int i = 0; i < NV; ++i) *reinterpret_cast<f32x4*>(share + i * 256 + lane * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < NV; ++i)
+        *reinterpret_cast<f32x4*>(shares + i * 256 + at.lane * 4) = f32x4{0.f, 0.f, 0.f, 0.f};
     const int t0 = static_cast<int>(blockIdx.x) * chunk;
-    const int t1 = min(T, t0 + chunk);
-    const uint64_t valid = valid_tokens(mask, t0, t1 - t0);
+    const int len = min(chunk, T - t0);
+    const float* rows = logits + static_cast<size_t>(t0) * E;
+    float* out = d_logits + static_cast<size_t>(t0) * E;
+    Row<NV, WPT> first;
+    Entry entry;
+    if (at.group < len) {
+        first.load(rows + static_cast<size_t>(at.group) * E, E, at.part, at.lane);
+        entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + at.group, K);
+    }
+    const uint64_t valid = valid_tokens(mask, t0, len);
+    const uint64_t share = at.share() & bit_range(0, len);
     const float g = d_loss[0] * temp / static_cast<float>(max(tokens[0], 1));
-    for (int t = t0 + wave; t < t1; t += kWaves) {
-        float* out = d_logits + static_cast<size_t>(t) * E;
+    for_rows(valid & share, rows, E, at.part, at.lane, first, at.group, [&](int t, Row<NV, WPT>& x) {
+        if (t != at.group) entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + t, K);
         int id = -1;
         float q = 0.f, logq = 0.f;
-        float d[NV][4];
-        if (!((valid >> (t - t0) & 1) &&
-              teacher_shares(t_ids, t_logits, t, K, E, score, inv_temp, id, q, logq))) {
-            if (accumulate) continue;
-#pragma unroll
-            for (int i = 0; i < NV; ++i)
-#pragma unroll
-                for (int j = 0; j < 4; ++j) d[i][j] = 0.f;
-            store_row(out, E, lane, d, false);
-            continue;
+        if (!teacher_shares(entry, E, score, inv_temp, id, q, logq)) {
+            x.fill(0.f);
+            if (!accumulate) x.store(out + static_cast<size_t>(t) * E, E, at.part, at.lane, false);
+            return;
         }
-        float x[NV][4], u[NV][4];
-        load_row(logits + static_cast<size_t>(t) * E, E, lane, x);
         // an expert named twice: every entry that names it holds the sum
         float same = 0.f;
         for (int j = 0; j < K; ++j) {
@@ -522,25 +714,37 @@ __global__ __launch_bounds__(kBlock) void distill_backward_kernel(
             const float oq = __int_as_float(__builtin_amdgcn_readlane(__float_as_int(q), j));
             if (other == id) same += oq;
         }
-        if (id >= 0) share[id] = same;
-        scale_row(x, inv_temp);
-        float slope[SIGMOID ? NV : 1][4];
-        if constexpr (SIGMOID) sigmoid_weights<NV, true>(x, u, slope);
-        else softmax_weights(x, u);
-        const float total = row_sum(u);
-        const float inv = total > 0.f ? 1.f / total : total == 0.f ? 0.f : total;
+        const bool mine = id >= 0 && (WPT == 1 || id / 256 % WPT == at.part);
+        if (mine) shares[place(id)] = same;
+        Row<NV, WPT> u, slope;
+        x.scale(inv_temp);
+        const float m = weight_origin(reduce.max(x.max()));
+        if constexpr (SIGMOID) sigmoid_weights<true>(x, fminf(m, 0.f), u, slope);
+        else softmax_weights(x, m, u);
+        float total[1] = {u.sum()};
+        reduce.sum(total);
+        const float inv = inverse(total[0]);
 #pragma unroll
         for (int i = 0; i < NV; ++i) {
-            const f32x4 sq = *reinterpret_cast<const f32x4*>(share + i * 256 + lane * 4);
+            const f32x4 sq = *reinterpret_cast<const f32x4*>(shares + i * 256 + at.lane * 4);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                d[i][j] = g * __builtin_fmaf(u[i][j], inv, -sq[j]);
-                if constexpr (SIGMOID) d[i][j] *= slope[i][j];
+                u.v[i][j] = g * __builtin_fmaf(u.v[i][j], inv, -sq[j]);
+                if constexpr (SIGMOID) u.v[i][j] *= slope.v[i][j];
             }
         }
-        if (id >= 0) share[id] = 0.f;
-        store_row(out, E, lane, d, accumulate);
-    }
+        if (mine) shares[place(id)] = 0.f;
+        u.store(out + static_cast<size_t>(t) * E, E, at.part, at.lane, accumulate);
+    });
+    if (accumulate) return;
+    Row<NV, WPT> zero;
+    zero.fill(0.f);
+    for (uint64_t bits = ~valid & share; bits; bits &= bits - 1)
+        zero.store(out + static_cast<size_t>(__builtin_ctzll(bits)) * E, E, at.part, at.lane, false);
+}
+
+inline bool distill_shape_ok(int T, int E) {
+    return T >= 0 && T <= MOE_MAX_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS;
 }
 
 inline bool score_ok(int score) { return score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX; }
@@ -550,7 +754,7 @@ inline bool score_ok(int score) { return score == MOE_SCORE_SIGMOID || score == 
 
 extern "C" size_t moe_balance_loss_workspace_bytes(int T, int E, int S) {
     using namespace moe;
-    return balance_shape_ok(T, E, S) ? plan_balance(T, E, S).bytes : 0;
+    return balance_shape_ok(T, E, S) && !balance_small(T, E, S) ? plan_balance(T, E, S).bytes : 0;
 }
 
 extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, const uint8_t* token_mask,
@@ -565,6 +769,18 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, co
     if (!losses || !counts || !probs || !tokens) return MOE_ERR_NULL_ARG;
     if (T > 0 && (!logits || !topk_ids || !token_mask)) return MOE_ERR_NULL_ARG;
     if (!all_aligned16(logits, topk_ids, token_mask, seq_offsets, losses, counts, probs, tokens)) return MOE_ERR_ALIGN;
+    const bool sigmoid = score == MOE_SCORE_SIGMOID;
+    if (balance_small(T, E, S))
+        return with_row_shape<kBalanceOneWave>(E, [&](auto nv, auto wpt) {
+            if constexpr (decltype(wpt)::value == 1) {
+                constexpr int NV = decltype(nv)::value;
+                auto kern = sigmoid ? balance_small_kernel<NV, true> : balance_small_kernel<NV, false>;
+                return launch(kern, dim3(1), dim3(kSmallGroups * kWave), sizeof(float) * kSmallGroups * E, stream, logits,
+                              topk_ids, token_mask, seq_offsets, T, E, k, S, losses, counts, probs, tokens);
+            } else {
+                return static_cast<int>(MOE_ERR_BAD_SHAPE);
+            }
+        });
     const BalancePlan p = plan_balance(T, E, S);
     if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
     char* ws = static_cast<char*>(workspace);
@@ -573,15 +789,22 @@ extern "C" int moe_balance_loss(const float* logits, const int32_t* topk_ids, co
     auto* part_n = reinterpret_cast<int32_t*>(ws + p.n);
     auto* part_z = reinterpret_cast<float*>(ws + p.z);
     auto* counter = reinterpret_cast<int32_t*>(ws + p.counter);
-    int st = with_row_vectors(E, [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
-        auto kern = score == MOE_SCORE_SIGMOID ? balance_partial_kernel<NV, true> : balance_partial_kernel<NV, false>;
-        return launch(kern, dim3(p.blocks > 0 ? p.blocks : 1), dim3(kBlock), 2 * sizeof(float) * E, stream, logits,
-                      topk_ids, token_mask, seq_offsets, T, E, k, S, p.chunk, part_probs, part_counts, part_n,
-                      part_z, counter);
+    const int st = with_row_shape<kBalanceOneWave>(E, [&](auto nv, auto wpt) {
+        constexpr int NV = decltype(nv)::value, WPT = decltype(wpt)::value;
+        constexpr int GROUPS = WPT > 1 ? 1 : kGroups;
+        const int groups = p.chunk == 1 ? 1 : GROUPS;
+        auto kern = groups == 1 ? (sigmoid ? balance_partial_kernel<NV, WPT, 1, true> : balance_partial_kernel<NV, WPT, 1, false>)
+                                : (sigmoid ? balance_partial_kernel<NV, WPT, GROUPS, true>
+                                           : balance_partial_kernel<NV, WPT, GROUPS, false>);
+        return launch(kern, dim3(p.blocks > 0 ? p.blocks : 1), dim3(WPT * groups * kWave),
+                      sizeof(float) * E * (WPT > 1 ? 1 : 1 + groups), stream, logits, topk_ids, token_mask, seq_offsets, T, E, k,
+                      S, p.chunk, part_probs, part_counts, part_n, part_z, counter);
     });
     if (st != MOE_OK) return st;
-    return launch(balance_reduce_kernel, dim3(S * p.col_blocks), dim3(kReduceBlock), 0, stream, part_probs,
+    auto reduce = p.cols == 16   ? balance_reduce_kernel<16>
+                  : p.cols == 64 ? balance_reduce_kernel<64>
+                                 : balance_reduce_kernel<256>;
+    return launch(reduce, dim3(S * p.col_blocks), dim3(kReduceBlock), 0, stream, part_probs,
                   part_counts, part_n, part_z, seq_offsets, T, E, k, S, p.chunk, p.col_blocks, losses, counts, probs,
                   tokens, reinterpret_cast<float*>(ws + p.dot), reinterpret_cast<float*>(ws + p.seq_z), counter);
 }
@@ -597,29 +820,20 @@ extern "C" int moe_balance_loss_backward(const float* d_losses, const float* log
     if (T == 0) return MOE_OK;
     if (!d_losses || !logits || !token_mask || !counts || !tokens || !d_logits) return MOE_ERR_NULL_ARG;
     if (!all_aligned16(d_losses, logits, token_mask, seq_offsets, counts, tokens, d_logits)) return MOE_ERR_ALIGN;
-    const int chunk = chunk_tokens(T);
-    return with_row_vectors(E, [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
-        auto kern = score == MOE_SCORE_SIGMOID ? balance_backward_kernel<NV, true> : balance_backward_kernel<NV, false>;
-        return launch(kern, dim3(ceil_div(T, chunk)), dim3(kBlock), 0, stream, d_losses, logits, token_mask,
-                      seq_offsets, counts, tokens, T, E, k, S, chunk, accumulate, d_logits);
+    const int chunk = chunk_tokens(T, E <= kBalanceOneWave, kTargetBlocks);
+    return with_row_shape<kBalanceOneWave>(E, [&](auto nv, auto wpt) {
+        constexpr int NV = decltype(nv)::value, WPT = decltype(wpt)::value;
+        auto kern = score == MOE_SCORE_SIGMOID ? balance_backward_kernel<NV, WPT, true>
+                                               : balance_backward_kernel<NV, WPT, false>;
+        return launch(kern, dim3(ceil_div(T, chunk)), dim3((WPT > 1 ? WPT : kGroups) * kWave), 0, stream, d_losses,
+                      logits, token_mask, seq_offsets, counts, tokens, T, E, k, S, chunk, accumulate, d_logits);
     });
 }
 
-namespace moe {
-namespace {
-
-inline bool distill_shape_ok(int T, int E) {
-    return T >= 0 && T <= MOE_MAX_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS;
-}
-
-}  // namespace
-}  // namespace moe
-
 extern "C" size_t moe_distill_loss_workspace_bytes(int T, int E) {
     using namespace moe;
-    if (!distill_shape_ok(T, E)) return 0;
-    const int blocks = ceil_div(T, chunk_tokens(T));
+    if (!distill_shape_ok(T, E) || small_batch(T, E)) return 0;
+    const int blocks = ceil_div(T, chunk_tokens(T, E <= kDistillOneWave, kDistillBlocks));
     return 2 * round256(sizeof(float) * (blocks > 0 ? blocks : 1));
 }
 
@@ -634,23 +848,37 @@ extern "C" int moe_distill_loss(const float* logits, const int32_t* teacher_ids,
     if (T > 0 && (!logits || !teacher_ids || !teacher_logits || !token_mask || !token_loss)) return MOE_ERR_NULL_ARG;
     if (!all_aligned16(logits, teacher_ids, teacher_logits, token_mask, loss, token_loss, tokens))
         return MOE_ERR_ALIGN;
+    const bool sigmoid = score == MOE_SCORE_SIGMOID;
+    const float inv_temp = 1.f / temperature, temp2 = temperature * temperature;
+    if (small_batch(T, E))
+        return with_row_shape<kDistillOneWave>(E, [&](auto nv, auto wpt) {
+            if constexpr (decltype(wpt)::value == 1) {
+                constexpr int NV = decltype(nv)::value <= 4 ? decltype(nv)::value : 4;   // up to kSmallExperts
+                auto kern = sigmoid ? distill_kernel<NV, 1, kSmallGroups, true> : distill_kernel<NV, 1, kSmallGroups, false>;
+                return launch(kern, dim3(1), dim3(kSmallGroups * kWave), 0, stream, logits, teacher_ids,
+                              teacher_logits, token_mask, inv_temp, temp2, T, E, K, kSmallTokens, token_loss, loss,
+                              tokens);
+            } else {
+                return static_cast<int>(MOE_ERR_BAD_SHAPE);
+            }
+        });
     if (!workspace || workspace_bytes < moe_distill_loss_workspace_bytes(T, E) || !aligned16(workspace))
         return MOE_ERR_WORKSPACE;
-    const int chunk = chunk_tokens(T);
+    const int chunk = chunk_tokens(T, E <= kDistillOneWave, kDistillBlocks);
     const int blocks = ceil_div(T, chunk);
     auto* part_loss = static_cast<float*>(workspace);
     auto* part_n = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + round256(sizeof(float) * (blocks > 0 ? blocks : 1)));
     if (T > 0) {
-        const int st = with_row_vectors(E, [&](auto nv) {
-            constexpr int NV = decltype(nv)::value;
-            auto kern = score == MOE_SCORE_SIGMOID ? distill_kernel<NV, true> : distill_kernel<NV, false>;
-            return launch(kern, dim3(blocks), dim3(kBlock), 0, stream, logits, teacher_ids, teacher_logits,
-                          token_mask, 1.f / temperature, temperature * temperature, T, E, K, chunk, token_loss,
-                          part_loss, part_n);
+        const int st = with_row_shape<kDistillOneWave>(E, [&](auto nv, auto wpt) {
+            constexpr int NV = decltype(nv)::value, WPT = decltype(wpt)::value, GROUPS = WPT > 1 ? 1 : kGroups;
+            auto kern = sigmoid ? distill_kernel<NV, WPT, GROUPS, true> : distill_kernel<NV, WPT, GROUPS, false>;
+            return launch(kern, dim3(blocks), dim3(WPT * GROUPS * kWave), 0, stream, logits, teacher_ids,
+                          teacher_logits, token_mask, inv_temp, temp2, T, E, K, chunk, token_loss, part_loss, part_n);
         });
         if (st != MOE_OK) return st;
     }
-    return launch(distill_reduce_kernel, dim3(1), dim3(kBlock), 0, stream, part_loss, part_n, blocks, loss, tokens);
+    return launch(distill_reduce_kernel, dim3(1), dim3(kDistillReduceBlock), 0, stream, part_loss, part_n, blocks,
+                  loss, tokens);
 }
 
 extern "C" int moe_distill_loss_backward(const float* d_loss, const float* logits, const int32_t* teacher_ids,
@@ -665,12 +893,13 @@ extern "C" int moe_distill_loss_backward(const float* d_loss, const float* logit
         return MOE_ERR_NULL_ARG;
     if (!all_aligned16(d_loss, logits, teacher_ids, teacher_logits, token_mask, tokens, d_logits))
         return MOE_ERR_ALIGN;
-    const int chunk = chunk_tokens(T);
-    return with_row_vectors(E, [&](auto nv) {
-        constexpr int NV = decltype(nv)::value;
-        auto kern = score == MOE_SCORE_SIGMOID ? distill_backward_kernel<NV, true> : distill_backward_kernel<NV, false>;
-        return launch(kern, dim3(ceil_div(T, chunk)), dim3(kBlock), sizeof(float) * kWaves * NV * 256, stream, d_loss,
-                      logits, teacher_ids, teacher_logits, token_mask, tokens, 1.f / temperature, temperature, T, E,
-                      K, chunk, accumulate, d_logits);
+    const int chunk = chunk_tokens(T, E <= kDistillOneWave, kDistillBlocks);
+    return with_row_shape<kDistillOneWave>(E, [&](auto nv, auto wpt) {
+        constexpr int NV = decltype(nv)::value, WPT = decltype(wpt)::value, WAVES = WPT > 1 ? WPT : kGroups;
+        auto kern = score == MOE_SCORE_SIGMOID ? distill_backward_kernel<NV, WPT, true>
+                                               : distill_backward_kernel<NV, WPT, false>;
+        return launch(kern, dim3(ceil_div(T, chunk)), dim3(WAVES * kWave), sizeof(float) * WAVES * NV * 256, stream,
+                      d_loss, logits, teacher_ids, teacher_logits, token_mask, tokens, 1.f / temperature, temperature,
+                      T, E, K, chunk, accumulate, d_logits);
     });
 }

@@ -1,10 +1,16 @@
-// A token's router logits held by one wave, and the router's distribution over
-// them, for the losses on the logits.
+// A token's router logits held by one wave or by several, and the router's
+// distribution over them, for the losses on the logits.
 //
-// The row of E logits is spread over the wave in vectors of four: lane l owns
-// columns 256 i + 4 l + (0..3) for i < NV (E <= 256 NV), so a load of the wave
-// covers 1 KB of the row. Columns from E on hold -inf, which weighs zero.
+// A row of E logits is spread over WPT waves in vectors of four: lane l of wave
+// w owns columns 256 (WPT i + w) + 4 l + (0..3) for i < NV (E <= 256 NV WPT), so
+// a load of a wave covers 1 KB of the row. Columns from E on hold -inf, which
+// weighs zero. Narrow rows take one wave, which needs no barrier; wide ones all
+// waves of a block, so that a row stays in few registers (with one wave for 4096
+// columns, 64 registers for each array, the balance loss of 4096 tokens took 92
+// us and its gradient 53; with four 17 and 22).
 #pragma once
+
+#include <type_traits>
 
 #include "common.hpp"
 #include "moe_training.h"
@@ -39,98 +45,164 @@ __device__ __forceinline__ float wave_max(float v) {
     return v;
 }
 
-template <int NV>
-__device__ __forceinline__ void load_row(const float* __restrict__ row, int E, int lane, float (&x)[NV][4]) {
+template <int NV, int WPT>
+struct Row {
+    float v[NV][4];
+
+    static __device__ __forceinline__ int column(int i, int wave, int lane) {
+        return (i * WPT + wave) * 256 + lane * 4;
+    }
+
+    __device__ __forceinline__ void fill(float f) {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = i * 256 + lane * 4;
-        if (c + 4 <= E) {
-            const f32x4 v = *reinterpret_cast<const f32x4_any*>(row + c);
+        for (int i = 0; i < NV; ++i)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[i][q] = v[q];
-        } else {
+            for (int q = 0; q < 4; ++q) v[i][q] = f;
+    }
+
+    __device__ __forceinline__ void scale(float f) {
 #pragma unroll
-            for (int q = 0; q < 4; ++q) x[i][q] = c + q < E ? row[c + q] : kNegInf;
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[i][q] *= f;
+    }
+
+    __device__ __forceinline__ void load(const float* __restrict__ row, int E, int wave, int lane) {
+#pragma unroll
+        for (int i = 0; i < NV; ++i) {
+            const int c = column(i, wave, lane);
+            if (c + 4 <= E) {
+                const f32x4 x = *reinterpret_cast<const f32x4_any*>(row + c);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[i][q] = x[q];
+            } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) v[i][q] = c + q < E ? row[c + q] : kNegInf;
+            }
         }
     }
-}
 
-// Writes the row, or adds it to what is there.
-template <int NV>
-__device__ __forceinline__ void store_row(float* __restrict__ row, int E, int lane, const float (&x)[NV][4],
-                                          bool accumulate) {
+    // Writes the row, or adds it to what is there.
+    __device__ __forceinline__ void store(float* __restrict__ row, int E, int wave, int lane, bool accumulate) const {
 #pragma unroll
-    for (int i = 0; i < NV; ++i) {
-        const int c = i * 256 + lane * 4;
-        if (c + 4 <= E) {
-            f32x4_any* p = reinterpret_cast<f32x4_any*>(row + c);
-            f32x4 v = {x[i][0], x[i][1], x[i][2], x[i][3]};
-            if (accumulate) v += *p;
-            *p = v;
-        } else {
+        for (int i = 0; i < NV; ++i) {
+            const int c = column(i, wave, lane);
+            if (c + 4 <= E) {
+                f32x4_any* p = reinterpret_cast<f32x4_any*>(row + c);
+                f32x4 x = {v[i][0], v[i][1], v[i][2], v[i][3]};
+                if (accumulate) x += *p;
+                *p = x;
+            } else {
 #pragma unroll
-            for (int q = 0; q < 4; ++q)
-                if (c + q < E) row[c + q] = accumulate ? row[c + q] + x[i][q] : x[i][q];
+                for (int q = 0; q < 4; ++q)
+                    if (c + q < E) row[c + q] = accumulate ? row[c + q] + v[i][q] : v[i][q];
+            }
         }
     }
-}
 
-template <int NV>
-__device__ __forceinline__ float row_max(const float (&x)[NV][4]) {
-    float m = kNegInf;
+    // This lane's part of the maximum and the sum.
+    __device__ __forceinline__ float max() const {
+        float m = kNegInf;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) m = fmaxf(m, v[i][q]);
+        return m;
+    }
+
+    __device__ __forceinline__ float sum() const {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s += v[i][q];
+        return s;
+    }
+
+    __device__ __forceinline__ float dot(const Row& o) const {
+        float s = 0.f;
+#pragma unroll
+        for (int i = 0; i < NV; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) s = __builtin_fmaf(v[i][q], o.v[i][q], s);
+        return s;
+    }
+};
+
+// Reductions over a row's waves. With several the waves meet in LDS: every wave
+// of the block calls, and two buffers alternate, so that a call costs one
+// barrier.
+template <int WPT>
+struct RowReduce {
+    float (*red)[WPT][4];   // [2][WPT][4] in LDS
+    int wave;
+    int buf = 0;
+
+    __device__ __forceinline__ float max(float m) {
+        m = wave_max(m);
+        if constexpr (WPT > 1) {
+            if (__lane_id() == 0) red[buf][wave][0] = m;
+            __syncthreads();
+            for (int w = 0; w < WPT; ++w) m = fmaxf(m, red[buf][w][0]);
+            buf ^= 1;
+        }
+        return m;
+    }
+
+    // Sums of N values, the waves' in order.
+    template <int N>
+    __device__ __forceinline__ void sum(float (&v)[N]) {
+        static_assert(N <= 4, "the buffer's width");
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = wave_sum(v[i]);
+        if constexpr (WPT > 1) {
+            if (__lane_id() == 0)
+#pragma unroll
+                for (int i = 0; i < N; ++i) red[buf][wave][i] = v[i];
+            __syncthreads();
+#pragma unroll
+            for (int i = 0; i < N; ++i) {
+                v[i] = red[buf][0][i];
+                for (int w = 1; w < WPT; ++w) v[i] += red[buf][w][i];
+            }
+            buf ^= 1;
+        }
+    }
+};
+
+// The maximum that weights are taken relative to: 0 for a row of -inf, whose
+// weights are then zero.
+__device__ __forceinline__ float weight_origin(float m) { return m == kNegInf ? 0.f : m; }
+
+// u = exp(x - m).
+template <int NV, int WPT>
+__device__ __forceinline__ void softmax_weights(const Row<NV, WPT>& x, float m, Row<NV, WPT>& u) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) m = fmaxf(m, x[i][q]);
-    return wave_max(m);
-}
-
-template <int NV>
-__device__ __forceinline__ float row_sum(const float (&x)[NV][4]) {
-    float s = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) s += x[i][q];
-    return wave_sum(s);
-}
-
-// u = exp(x - max x), returning the maximum (0 for a row of -inf, whose u are
-// then zero).
-template <int NV>
-__device__ __forceinline__ float softmax_weights(const float (&x)[NV][4], float (&u)[NV][4]) {
-    float m = row_max(x);
-    if (m == kNegInf) m = 0.f;
-#pragma unroll
-    for (int i = 0; i < NV; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) u[i][q] = exp_fast(x[i][q] - m);
-    return m;
+        for (int q = 0; q < 4; ++q) u.v[i][q] = exp_fast(x.v[i][q] - m);
 }
 
 // The sigmoid s of x, relative to the row's largest: with e = exp(-|x|),
 //   s = exp(min(x, 0)) / (1 + e),   1 - s = exp(-max(x, 0)) / (1 + e),
-// u = exp(min(x, 0) - m) / (1 + e), m = max min(x, 0) <= 0, so that a row
-// whose every s underflows keeps its proportions. Returns m (0 when a logit is
-// positive, and then u = s with one exponential).
-template <int NV, bool SLOPE>
-__device__ __forceinline__ float sigmoid_weights(const float (&x)[NV][4], float (&u)[NV][4],
-                                                 float (&slope)[SLOPE ? NV : 1][4]) {
-    float m = fminf(row_max(x), 0.f);
-    if (m == kNegInf) m = 0.f;
+// u = exp(min(x, 0) - m) / (1 + e), m = min(max x, 0), so that a row whose every
+// s underflows keeps its proportions (m = 0 when a logit is positive, and then
+// u = s with one exponential).
+template <bool SLOPE, int NV, int WPT>
+__device__ __forceinline__ void sigmoid_weights(const Row<NV, WPT>& x, float m, Row<NV, WPT>& u,
+                                                Row<NV, WPT>& slope) {
 #pragma unroll
     for (int i = 0; i < NV; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
-            const float v = x[i][q];
+            const float v = x.v[i][q];
             const float e = exp_fast(-fabsf(v));
             const float r = __builtin_amdgcn_rcpf(1.f + e);
             const float er = e * r;
-            u[i][q] = v > 0.f ? r : er;
-            if constexpr (SLOPE) slope[i][q] = v > 0.f ? er : r;
-            if (m < 0.f) u[i][q] = exp_fast(v - m) * r;   // every logit is negative
+            u.v[i][q] = v > 0.f ? r : er;
+            if constexpr (SLOPE) slope.v[i][q] = v > 0.f ? er : r;
+            if (m < 0.f) u.v[i][q] = exp_fast(v - m) * r;   // every logit is negative
         }
-    return m;
 }
 
 // log of the score of one logit (the sigmoid's, or the logit itself).
@@ -168,16 +240,24 @@ __device__ __forceinline__ int find_sequence(const int32_t* __restrict__ off, in
     return t < end ? lo : -1;
 }
 
-// Picks NV for E experts and calls f with it as a constant.
-template <typename F>
-inline int with_row_vectors(int E, F&& f) {
-    if (E <= 256) return f(std::integral_constant<int, 1>());
-    if (E <= 512) return f(std::integral_constant<int, 2>());
-    if (E <= 1024) return f(std::integral_constant<int, 4>());
-    if (E <= 1536) return f(std::integral_constant<int, 6>());
-    if (E <= 2048) return f(std::integral_constant<int, 8>());
-    if (E <= 2560) return f(std::integral_constant<int, 10>());
-    return f(std::integral_constant<int, 16>());
+// Calls f with the vectors per lane and the waves per row that E experts take.
+// ONE_WAVE_MAX: the widest row for one wave, where what a pass keeps per column
+// fits its registers.
+template <int ONE_WAVE_MAX, typename F>
+inline int with_row_shape(int E, F&& f) {
+    using std::integral_constant;
+    using one = integral_constant<int, 1>;
+    if (E <= 256) return f(one(), one());
+    if (E <= 512) return f(integral_constant<int, 2>(), one());
+    if (E <= 1024) return f(integral_constant<int, 4>(), one());
+    if constexpr (ONE_WAVE_MAX >= 2560) {
+        if (E <= 1536) return f(integral_constant<int, 6>(), one());
+        if (E <= 2560) return f(integral_constant<int, 10>(), one());
+    } else {
+        if (E <= 2048) return f(integral_constant<int, 2>(), integral_constant<int, 4>());
+        if (E <= 2560) return f(integral_constant<int, 2>(), integral_constant<int, 5>());
+    }
+    return f(integral_constant<int, 4>(), integral_constant<int, 4>());
 }
 
 }  // namespace moe

@@ -22,6 +22,17 @@ _I32 = (torch.int32,)
 _MASK = (torch.uint8, torch.bool)
 
 
+def _out(t, name, like, dtype, shape, dev):
+    """An output: the caller's, checked, or a new one (from `like`, a tensor on
+    dev, where that has the type: new_empty is the cheaper allocation)."""
+    if t is None:
+        if like is not None and like.dtype == dtype:
+            return like.new_empty(shape)
+        return torch.empty(shape, dtype=dtype, device=dev)
+    _need(t, name, _BF16 if dtype == torch.bfloat16 else (dtype,), shape, dev)
+    return t
+
+
 def _table(logits, token_mask):
     """Checks [T,E] logits and their mask; returns (device, T, E)."""
     dev = logits.device
@@ -52,7 +63,7 @@ def _gradient(d_logits, accumulate, T, E, dev):
     if d_logits is None:
         if accumulate:
             raise ValueError("accumulate needs d_logits to add to")
-        d_logits = torch.empty((T, E), dtype=torch.float32, device=dev)
+        return torch.empty((T, E), dtype=torch.float32, device=dev)
     _need(d_logits, "d_logits", _F32, (T, E), dev)
     return d_logits
 
@@ -74,14 +85,10 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError("topk_ids must be [T,k] with logits' T")
     k = topk_ids.shape[1]
-    losses = torch.empty(2, dtype=torch.float32, device=dev) if losses is None else losses
-    counts = torch.empty((S, E), dtype=torch.int32, device=dev) if counts is None else counts
-    probs = torch.empty((S, E), dtype=torch.float32, device=dev) if probs is None else probs
-    tokens = torch.empty(S + 2, dtype=torch.int32, device=dev) if tokens is None else tokens
-    _need(losses, "losses", _F32, (2,), dev)
-    _need(counts, "counts", _I32, (S, E), dev)
-    _need(probs, "probs", _F32, (S, E), dev)
-    _need(tokens, "tokens", _I32, (S + 2,), dev)
+    losses = _out(losses, "losses", logits, torch.float32, (2,), dev)
+    counts = _out(counts, "counts", topk_ids, torch.int32, (S, E), dev)
+    probs = _out(probs, "probs", logits, torch.float32, (S, E), dev)
+    tokens = _out(tokens, "tokens", topk_ids, torch.int32, (S + 2,), dev)
     workspace, ws_len = _workspace(workspace, balance_loss_workspace_bytes(T, E, S), dev)
     _check("moe_balance_loss", lib().moe_balance_loss(
         _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(seq_offsets), score, T, E, k, S, _ptr(losses),
@@ -129,12 +136,9 @@ def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     fp32, token_loss [T] fp32, tokens [1] int32)."""
     dev, T, E = _table(logits, token_mask)
     K = _teacher(teacher_ids, teacher_logits, T, dev)
-    loss = torch.empty(1, dtype=torch.float32, device=dev) if loss is None else loss
-    token_loss = torch.empty(T, dtype=torch.float32, device=dev) if token_loss is None else token_loss
-    tokens = torch.empty(1, dtype=torch.int32, device=dev) if tokens is None else tokens
-    _need(loss, "loss", _F32, (1,), dev)
-    _need(token_loss, "token_loss", _F32, (T,), dev)
-    _need(tokens, "tokens", _I32, (1,), dev)
+    loss = _out(loss, "loss", logits, torch.float32, (1,), dev)
+    token_loss = _out(token_loss, "token_loss", logits, torch.float32, (T,), dev)
+    tokens = _out(tokens, "tokens", teacher_ids, torch.int32, (1,), dev)
     workspace, ws_len = _workspace(workspace, distill_loss_workspace_bytes(T, E), dev)
     _check("moe_distill_loss", lib().moe_distill_loss(
         _ptr(logits), _ptr(teacher_ids), _ptr(teacher_logits), _ptr(token_mask), score, float(temperature), T, E, K,
@@ -196,8 +200,7 @@ def route_backward(d_topk_w: Optional[torch.Tensor], hidden: Optional[torch.Tens
         _need(topk_w, "topk_w", _F32, (T, k), dev)
     if d_aux is not None:
         _need(d_aux, "d_aux", _F32, (T, E), dev)
-    d_logits = torch.empty((T, E), dtype=torch.float32, device=dev) if d_logits is None else d_logits
-    _need(d_logits, "d_logits", _F32, (T, E), dev)
+    d_logits = _out(d_logits, "d_logits", table, torch.float32, (T, E), dev)
     H, dtype = 16, MOE_DTYPE_BF16
     if hidden is None:
         need_hidden = need_W = False
@@ -209,13 +212,14 @@ def route_backward(d_topk_w: Optional[torch.Tensor], hidden: Optional[torch.Tens
         dtype = MOE_DTYPE_F32 if hidden.dtype == torch.float32 else MOE_DTYPE_BF16
     if need_hidden:
         _need(W, "W", _F32, (E, H), dev)
-        d_hidden = torch.empty_like(hidden) if d_hidden is None else d_hidden
-        _need(d_hidden, "d_hidden", _F32 if dtype == MOE_DTYPE_F32 else _BF16, (T, H), dev)
+        if d_hidden is None:
+            d_hidden = torch.empty_like(hidden)
+        else:
+            _need(d_hidden, "d_hidden", _F32 if dtype == MOE_DTYPE_F32 else _BF16, (T, H), dev)
     else:
         d_hidden = None
     if need_W:
-        d_W = torch.empty((E, H), dtype=torch.float32, device=dev) if d_W is None else d_W
-        _need(d_W, "d_W", _F32, (E, H), dev)
+        d_W = _out(d_W, "d_W", table, torch.float32, (E, H), dev)
     else:
         d_W = None
     workspace, ws_len = _workspace(workspace, route_backward_workspace_bytes(T, H, E, dtype, hidden is None), dev)
@@ -254,16 +258,9 @@ def combine_backward(d_out: torch.Tensor, expert_out: torch.Tensor, slots: torch
     _need(d_out, "d_out", _BF16, (T, H), dev)
     _need(topk_w, "topk_w", _F32, (T, k), dev)
     _need(norm_w, "norm_w", _F32, (H,), dev)
-    if d_expert_out is None:
-        d_expert_out = torch.empty((R, H), dtype=torch.bfloat16, device=dev)
-    d_topk_w = torch.empty((T, k), dtype=torch.float32, device=dev) if d_topk_w is None else d_topk_w
-    _need(d_expert_out, "d_expert_out", _BF16, (R, H), dev)
-    _need(d_topk_w, "d_topk_w", _F32, (T, k), dev)
-    if need_norm_w:
-        d_norm_w = torch.empty(H, dtype=torch.float32, device=dev) if d_norm_w is None else d_norm_w
-        _need(d_norm_w, "d_norm_w", _F32, (H,), dev)
-    else:
-        d_norm_w = None
+    d_expert_out = _out(d_expert_out, "d_expert_out", d_out, torch.bfloat16, (R, H), dev)
+    d_topk_w = _out(d_topk_w, "d_topk_w", topk_w, torch.float32, (T, k), dev)
+    d_norm_w = _out(d_norm_w, "d_norm_w", topk_w, torch.float32, (H,), dev) if need_norm_w else None
     workspace, ws_len = _workspace(workspace, combine_backward_workspace_bytes(T, R, H), dev)
     _check("moe_combine_backward", lib().moe_combine_backward(
         _ptr(d_out), _ptr(expert_out), R, _ptr(slots), _ptr(topk_w), _ptr(norm_w), float(gain_center), float(eps),

@@ -48,10 +48,12 @@ def test_balance_loss_rejects_before_launch(lib):
     for name in ("logits", "ids", "mask", "losses", "counts", "probs", "tokens"):
         assert call(**{name: None}) == -1, name
         assert call(**{name: ODD}) == -7, name
-    assert call(ws=None) == -4
-    need = m.balance_loss_workspace_bytes(4, 16, 3)
+    need = m.balance_loss_workspace_bytes(400, 16, 3)
     assert need % 256 == 0 and need >= 2 * 4 * 16 * 4
-    assert call(wsb=need - 1) == -4
+    assert call(T=400, ws=None) == -4 and call(T=400, wsb=need - 1) == -4
+    assert call(T=400, ws=V((1 << 20) + 8)) == -4
+    assert m.balance_loss_workspace_bytes(4, 16, 3) == 0          # one block, no workspace
+    assert m.balance_loss_workspace_bytes(4, 16, 64) > 0 and m.balance_loss_workspace_bytes(4, 4096, 1) > 0
     assert m.balance_loss_workspace_bytes(4, 0, 3) == 0 and m.balance_loss_workspace_bytes(-1, 4, 3) == 0
 
 
@@ -80,7 +82,9 @@ def test_distill_loss_rejects_before_launch(lib):
     for name in ("logits", "ids", "z", "mask", "loss", "each", "tokens"):
         assert call(**{name: None}) == -1, name
         assert call(**{name: ODD}) == -7, name
-    assert call(ws=None) == -4 and call(wsb=m.distill_loss_workspace_bytes(4, 16) - 1) == -4
+    need = m.distill_loss_workspace_bytes(400, 16)
+    assert call(T=400, ws=None) == -4 and call(T=400, wsb=need - 1) == -4
+    assert m.distill_loss_workspace_bytes(4, 16) == 0 and m.distill_loss_workspace_bytes(4, 4096) > 0
     assert m.distill_loss_workspace_bytes(4, 4097) == 0
 
 
