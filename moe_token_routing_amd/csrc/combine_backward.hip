@@ -14,7 +14,7 @@
 // in registers for its k rows and each row in registers between the sums and
 // the gradient. Blocks are persistent over tokens, so that the gain's gradient
 // is summed in registers and only one row of partial sums per block is
-// written; a last kernel adds those in block order.
+// written; a last kernel adds those in block order, beside the mending below.
 //
 // Rows and slots need not match one to one. The main kernel writes every named
 // row's gradient and, for each row, a slot that names it (`owner`: any of them
@@ -407,8 +407,32 @@ __device__ __forceinline__ void repeated_row(const u32x4* __restrict__ d_out, co
     }
 }
 
-// Rows and slots [8 w, 8 w + 8) by wave w: zeros for rows without a slot, the
-// sum for rows with several. Eight, so that the unnamed rows at a dispatch's end
+constexpr int kGainCols = 16;
+constexpr int kGainGroups = kSmallBlock / kGainCols;
+
+// Columns [16 b, 16 b + 16) of the blocks' partial gain gradients, 16 groups of
+// threads over them.
+__device__ __forceinline__ void reduce_gain(const float* __restrict__ part, int rows, int H, int b,
+                                            float* __restrict__ d_norm_w) {
+    __shared__ float s[kGainGroups][kGainCols + 1];
+    const int col = threadIdx.x % kGainCols, group = threadIdx.x / kGainCols;
+    const int c = b * kGainCols + col;
+    float v = 0.f;
+    if (c < H) {
+#pragma unroll 16
+        for (int r = group; r < rows; r += kGainGroups) v += part[static_cast<size_t>(r) * H + c];
+    }
+    s[group][col] = v;
+    __syncthreads();
+    if (group == 0 && c < H) {
+        for (int g = 1; g < kGainGroups; ++g) v += s[g][col];
+        d_norm_w[c] = v;
+    }
+}
+
+// The first gain_blocks blocks add up the gain's gradient. The others take rows
+// and slots [8 w, 8 w + 8) by wave w: zeros for rows without a slot, the sum
+// for rows with several. Eight, so that the unnamed rows at a dispatch's end
 // spread over many waves. The first of a row's slots that finds another one as
 // its owner claims the row by turning the owner into its complement; the
 // complement still says who the owner is.
@@ -417,12 +441,18 @@ constexpr int kRowsPerWave = 8;
 __global__ __launch_bounds__(kSmallBlock) void combine_backward_rows_kernel(
     const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
     const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
-    float gain_center, float eps, int n, int H, int k, int32_t* owner, u32x4* __restrict__ d_rows) {
+    float gain_center, float eps, int n, int H, int k, int32_t* owner, u32x4* __restrict__ d_rows,
+    const float* __restrict__ part_gain, int parts, int gain_blocks, float* __restrict__ d_norm_w) {
+    if (static_cast<int>(blockIdx.x) < gain_blocks) {
+        reduce_gain(part_gain, parts, H, blockIdx.x, d_norm_w);
+        return;
+    }
     const int lane = __lane_id();
     const int nvec = H >> 3;
     const long long items = R > n ? R : n;
-    const long long stride = static_cast<long long>(gridDim.x) * (kSmallBlock / kWave) * kRowsPerWave;
-    for (long long i0 = (static_cast<long long>(blockIdx.x) * (kSmallBlock / kWave) + threadIdx.x / kWave) * kRowsPerWave;
+    const long long block = static_cast<long long>(blockIdx.x) - gain_blocks;
+    const long long stride = (static_cast<long long>(gridDim.x) - gain_blocks) * (kSmallBlock / kWave) * kRowsPerWave;
+    for (long long i0 = (block * (kSmallBlock / kWave) + threadIdx.x / kWave) * kRowsPerWave;
          i0 < items; i0 += stride) {
         const long long i = i0 + lane;
         bool unnamed = false, repeated = false;
@@ -454,28 +484,6 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_rows_kernel(
             todo &= todo - 1;
             repeated_row(d_out, expert_out, slots, topk_w, norm_w, gain_center, eps, n, H, k, row, d_rows);
         }
-    }
-}
-
-constexpr int kGainCols = 32;
-constexpr int kGainGroups = 32;
-
-// Columns [32 b, 32 b + 32) of the partial rows, 32 groups of threads over them.
-__global__ __launch_bounds__(kGainCols* kGainGroups) void gain_reduce_kernel(const float* __restrict__ part, int rows,
-                                                                              int H, float* __restrict__ d_norm_w) {
-    __shared__ float s[kGainGroups][kGainCols + 1];
-    const int col = threadIdx.x % kGainCols, group = threadIdx.x / kGainCols;
-    const int c = blockIdx.x * kGainCols + col;
-    float v = 0.f;
-    if (c < H) {
-#pragma unroll 4
-        for (int r = group; r < rows; r += kGainGroups) v += part[static_cast<size_t>(r) * H + c];
-    }
-    s[group][col] = v;
-    __syncthreads();
-    if (group == 0 && c < H) {
-        for (int g = 1; g < kGainGroups; ++g) v += s[g][col];
-        d_norm_w[c] = v;
     }
 }
 
@@ -569,15 +577,13 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
                             : run(combine_backward_kernel<4, kWideBlock, kWideBlock>);
         if (st != MOE_OK) return st;
     }
-    if (R > 0) {
-        const int n = T * k;
-        const long long blocks = ceil_div(R > n ? R : n, kRowsPerWave * (kSmallBlock / kWave));
-        const long long most = 16ll * device_cu_count();
-        st = launch(combine_backward_rows_kernel, dim3(static_cast<unsigned>(blocks < most ? blocks : most)),
-                    dim3(kSmallBlock), 0, stream, y, x, R, slots, topk_w, norm_w, gain_center, eps, n, H, k, owner, dx);
-        if (st != MOE_OK) return st;
-    }
-    if (!d_norm_w) return MOE_OK;
-    return launch(gain_reduce_kernel, dim3(ceil_div(H, kGainCols)), dim3(kGainCols * kGainGroups), 0, stream, part,
-                  T > 0 ? p.grid : 0, H, d_norm_w);
+    if (R == 0 && !d_norm_w) return MOE_OK;
+    const int n = T * k;
+    const int gain_blocks = d_norm_w ? ceil_div(H, kGainCols) : 0;
+    const long long blocks = R > 0 ? ceil_div(R > n ? R : n, kRowsPerWave * (kSmallBlock / kWave)) : 0;
+    const long long most = 16ll * device_cu_count();
+    return launch(combine_backward_rows_kernel,
+                  dim3(gain_blocks + static_cast<unsigned>(blocks < most ? blocks : most)), dim3(kSmallBlock), 0, stream,
+                  y, x, R, slots, topk_w, norm_w, gain_center, eps, n, H, k, owner, dx, part, T > 0 ? p.grid : 0,
+                  gain_blocks, d_norm_w);
 }

@@ -12,7 +12,7 @@ from typing import Optional
 
 import torch
 
-from . import MOE_DTYPE_BF16, MOE_DTYPE_F32, _BF16, _check, _need, _ptr, _stream, _workspace, lib
+from . import MOE_DTYPE_BF16, MOE_DTYPE_F32, _BF16, _check, _need, _ptr, _stream, lib
 
 MOE_SCORE_SIGMOID = 0
 MOE_SCORE_SOFTMAX = 1
@@ -22,15 +22,29 @@ _I32 = (torch.int32,)
 _MASK = (torch.uint8, torch.bool)
 
 
-def _out(t, name, like, dtype, shape, dev):
-    """An output: the caller's, checked, or a new one (from `like`, a tensor on
-    dev, where that has the type: new_empty is the cheaper allocation)."""
+def _new(shape, dtype, dev):
+    # empty_strided is torch's cheapest allocation (1.2 us against 1.6 for empty)
+    strides = (1,) if len(shape) == 1 else (shape[1], 1)
+    return torch.empty_strided(shape, strides, dtype=dtype, device=dev)
+
+
+def _out(t, name, dtype, shape, dev):
+    """An output: the caller's, checked, or a new one."""
     if t is None:
-        if like is not None and like.dtype == dtype:
-            return like.new_empty(shape)
-        return torch.empty(shape, dtype=dtype, device=dev)
+        return _new(shape, dtype, dev)
     _need(t, name, _BF16 if dtype == torch.bfloat16 else (dtype,), shape, dev)
     return t
+
+
+def _scratch(workspace, nbytes, dev):
+    """The workspace's pointer and length; a new one where none is given."""
+    if workspace is None:
+        if nbytes == 0:
+            return None, None, 0
+        workspace = _new((nbytes,), torch.uint8, dev)
+    elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on %s" % dev)
+    return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
 
 
 def _table(logits, token_mask):
@@ -63,7 +77,7 @@ def _gradient(d_logits, accumulate, T, E, dev):
     if d_logits is None:
         if accumulate:
             raise ValueError("accumulate needs d_logits to add to")
-        return torch.empty((T, E), dtype=torch.float32, device=dev)
+        return _new((T, E), torch.float32, dev)
     _need(d_logits, "d_logits", _F32, (T, E), dev)
     return d_logits
 
@@ -85,14 +99,14 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch
     if topk_ids.dim() != 2 or topk_ids.shape[0] != T:
         raise ValueError("topk_ids must be [T,k] with logits' T")
     k = topk_ids.shape[1]
-    losses = _out(losses, "losses", logits, torch.float32, (2,), dev)
-    counts = _out(counts, "counts", topk_ids, torch.int32, (S, E), dev)
-    probs = _out(probs, "probs", logits, torch.float32, (S, E), dev)
-    tokens = _out(tokens, "tokens", topk_ids, torch.int32, (S + 2,), dev)
-    workspace, ws_len = _workspace(workspace, balance_loss_workspace_bytes(T, E, S), dev)
+    losses = _out(losses, "losses", torch.float32, (2,), dev)
+    counts = _out(counts, "counts", torch.int32, (S, E), dev)
+    probs = _out(probs, "probs", torch.float32, (S, E), dev)
+    tokens = _out(tokens, "tokens", torch.int32, (S + 2,), dev)
+    workspace, ws, ws_len = _scratch(workspace, balance_loss_workspace_bytes(T, E, S), dev)
     _check("moe_balance_loss", lib().moe_balance_loss(
-        _ptr(logits), _ptr(topk_ids), _ptr(token_mask), _ptr(seq_offsets), score, T, E, k, S, _ptr(losses),
-        _ptr(counts), _ptr(probs), _ptr(tokens), _ptr(workspace), ws_len, _stream(dev)))
+        logits.data_ptr(), topk_ids.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), score, T, E, k, S,
+        losses.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(), ws, ws_len, _stream(dev)))
     return losses, counts, probs, tokens
 
 
@@ -110,8 +124,8 @@ def balance_loss_backward(d_losses: torch.Tensor, logits: torch.Tensor, token_ma
     _need(tokens, "tokens", _I32, (S + 2,), dev)
     d_logits = _gradient(d_logits, accumulate, T, E, dev)
     _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        _ptr(d_losses), _ptr(logits), _ptr(token_mask), _ptr(seq_offsets), _ptr(counts), _ptr(tokens), score, T, E,
-        k, S, int(bool(accumulate)), _ptr(d_logits), _stream(dev)))
+        d_losses.data_ptr(), logits.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), counts.data_ptr(),
+        tokens.data_ptr(), score, T, E, k, S, int(bool(accumulate)), d_logits.data_ptr(), _stream(dev)))
     return d_logits
 
 
@@ -136,13 +150,14 @@ def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     fp32, token_loss [T] fp32, tokens [1] int32)."""
     dev, T, E = _table(logits, token_mask)
     K = _teacher(teacher_ids, teacher_logits, T, dev)
-    loss = _out(loss, "loss", logits, torch.float32, (1,), dev)
-    token_loss = _out(token_loss, "token_loss", logits, torch.float32, (T,), dev)
-    tokens = _out(tokens, "tokens", teacher_ids, torch.int32, (1,), dev)
-    workspace, ws_len = _workspace(workspace, distill_loss_workspace_bytes(T, E), dev)
+    loss = _out(loss, "loss", torch.float32, (1,), dev)
+    token_loss = _out(token_loss, "token_loss", torch.float32, (T,), dev)
+    tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
+    workspace, ws, ws_len = _scratch(workspace, distill_loss_workspace_bytes(T, E), dev)
     _check("moe_distill_loss", lib().moe_distill_loss(
-        _ptr(logits), _ptr(teacher_ids), _ptr(teacher_logits), _ptr(token_mask), score, float(temperature), T, E, K,
-        _ptr(loss), _ptr(token_loss), _ptr(tokens), _ptr(workspace), ws_len, _stream(dev)))
+        logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(), token_mask.data_ptr(), score,
+        float(temperature), T, E, K, loss.data_ptr(), token_loss.data_ptr(), tokens.data_ptr(), ws, ws_len,
+        _stream(dev)))
     return loss, token_loss, tokens
 
 
@@ -158,8 +173,9 @@ def distill_loss_backward(d_loss: torch.Tensor, logits: torch.Tensor, teacher_id
     _scalars(tokens, "tokens", 1, _I32, dev)
     d_logits = _gradient(d_logits, accumulate, T, E, dev)
     _check("moe_distill_loss_backward", lib().moe_distill_loss_backward(
-        _ptr(d_loss), _ptr(logits), _ptr(teacher_ids), _ptr(teacher_logits), _ptr(token_mask), _ptr(tokens), score,
-        float(temperature), T, E, K, int(bool(accumulate)), _ptr(d_logits), _stream(dev)))
+        d_loss.data_ptr(), logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+        token_mask.data_ptr(), tokens.data_ptr(), score, float(temperature), T, E, K, int(bool(accumulate)),
+        d_logits.data_ptr(), _stream(dev)))
     return d_logits
 
 
@@ -200,7 +216,7 @@ def route_backward(d_topk_w: Optional[torch.Tensor], hidden: Optional[torch.Tens
         _need(topk_w, "topk_w", _F32, (T, k), dev)
     if d_aux is not None:
         _need(d_aux, "d_aux", _F32, (T, E), dev)
-    d_logits = _out(d_logits, "d_logits", table, torch.float32, (T, E), dev)
+    d_logits = _out(d_logits, "d_logits", torch.float32, (T, E), dev)
     H, dtype = 16, MOE_DTYPE_BF16
     if hidden is None:
         need_hidden = need_W = False
@@ -219,13 +235,13 @@ def route_backward(d_topk_w: Optional[torch.Tensor], hidden: Optional[torch.Tens
     else:
         d_hidden = None
     if need_W:
-        d_W = _out(d_W, "d_W", table, torch.float32, (E, H), dev)
+        d_W = _out(d_W, "d_W", torch.float32, (E, H), dev)
     else:
         d_W = None
-    workspace, ws_len = _workspace(workspace, route_backward_workspace_bytes(T, H, E, dtype, hidden is None), dev)
+    workspace, ws, ws_len = _scratch(workspace, route_backward_workspace_bytes(T, H, E, dtype, hidden is None), dev)
     _check("moe_route_backward", lib().moe_route_backward(
         _ptr(d_topk_w), _ptr(d_aux), _ptr(hidden), dtype, _ptr(W), _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
-        _ptr(token_mask), float(scale), T, H, E, k, _ptr(d_logits), _ptr(d_hidden), _ptr(d_W), _ptr(workspace),
+        token_mask.data_ptr(), float(scale), T, H, E, k, d_logits.data_ptr(), _ptr(d_hidden), _ptr(d_W), ws,
         ws_len, _stream(dev)))
     return d_logits, d_hidden, d_W
 
@@ -258,11 +274,12 @@ def combine_backward(d_out: torch.Tensor, expert_out: torch.Tensor, slots: torch
     _need(d_out, "d_out", _BF16, (T, H), dev)
     _need(topk_w, "topk_w", _F32, (T, k), dev)
     _need(norm_w, "norm_w", _F32, (H,), dev)
-    d_expert_out = _out(d_expert_out, "d_expert_out", d_out, torch.bfloat16, (R, H), dev)
-    d_topk_w = _out(d_topk_w, "d_topk_w", topk_w, torch.float32, (T, k), dev)
-    d_norm_w = _out(d_norm_w, "d_norm_w", topk_w, torch.float32, (H,), dev) if need_norm_w else None
-    workspace, ws_len = _workspace(workspace, combine_backward_workspace_bytes(T, R, H), dev)
+    d_expert_out = _out(d_expert_out, "d_expert_out", torch.bfloat16, (R, H), dev)
+    d_topk_w = _out(d_topk_w, "d_topk_w", torch.float32, (T, k), dev)
+    d_norm_w = _out(d_norm_w, "d_norm_w", torch.float32, (H,), dev) if need_norm_w else None
+    workspace, ws, ws_len = _scratch(workspace, combine_backward_workspace_bytes(T, R, H), dev)
     _check("moe_combine_backward", lib().moe_combine_backward(
-        _ptr(d_out), _ptr(expert_out), R, _ptr(slots), _ptr(topk_w), _ptr(norm_w), float(gain_center), float(eps),
-        T, H, k, _ptr(d_expert_out), _ptr(d_topk_w), _ptr(d_norm_w), _ptr(workspace), ws_len, _stream(dev)))
+        d_out.data_ptr(), expert_out.data_ptr(), R, slots.data_ptr(), topk_w.data_ptr(), norm_w.data_ptr(),
+        float(gain_center), float(eps), T, H, k, d_expert_out.data_ptr(), d_topk_w.data_ptr(), _ptr(d_norm_w), ws,
+        ws_len, _stream(dev)))
     return d_expert_out, d_topk_w, d_norm_w
