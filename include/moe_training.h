@@ -191,7 +191,7 @@ int moe_distill_loss_backward(const float* d_loss, const float* logits, const in
  *   d_W        [E,H] FP32 output, or NULL: not wanted.
  *   workspace  at least moe_route_backward_workspace_bytes(T, H, E,
  *              hidden_dtype, logits_in) bytes, 256-byte aligned (may be NULL
- *              when that is 0).
+ *              when that is 0: logits-in mode, or too few tokens to need any).
  * Errors: NULL_ARG, BAD_SHAPE, BAD_DTYPE, BAD_ARG (non-finite scale), ALIGN,
  * WORKSPACE, HIP.
  */

@@ -25,6 +25,7 @@
 // n of MFMA j holds column 4 n + j), which costs one v_perm per two elements and
 // makes a lane's four results of a row adjacent in memory.
 #include <cmath>
+#include <type_traits>
 
 #include "launch.hpp"
 
@@ -133,6 +134,76 @@ __device__ __forceinline__ void split_rows(const SplitArgs& a, int H, long long 
     }
 }
 
+// The picks of 32 tokens from t0 on, eight threads a token and up to four picks a
+// thread, and what they add to the gradient of the logits in columns [e0, e1).
+struct Picks {
+    static constexpr int N = MOE_MAX_TOPK / 8;
+    int id[N];
+    float w[N], dw[N];
+
+    // valid: bit r is set when token t0 + r is
+    __device__ __forceinline__ void load(const PrepArgs& p, int t0, uint32_t valid) {
+        const int r = threadIdx.x >> 3, sub = threadIdx.x & 7;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const int j = sub + 8 * q;
+            const size_t at = static_cast<size_t>(t0 + r) * p.k + j;
+            id[q] = -1;
+            w[q] = dw[q] = 0.f;
+            if (j < p.k && (valid >> r & 1)) {
+                const int e = p.ids[at];
+                if (e >= 0 && e < p.E) {
+                    id[q] = e;
+                    w[q] = p.topk_w[at];
+                    dw[q] = p.d_topk_w[at];
+                }
+            }
+        }
+    }
+
+    // w (1 - s) (dw - sum w dw) of each pick into LDS; a barrier must follow
+    __device__ __forceinline__ void values(const PrepArgs& p, int t0, int e0, int e1,
+                                           int32_t (*pick_id)[MOE_MAX_TOPK], float (*pick_v)[MOE_MAX_TOPK]) const {
+        const int r = threadIdx.x >> 3, sub = threadIdx.x & 7;
+        float l[N], s = 0.f;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            s = __builtin_fmaf(w[q], dw[q], s);
+            l[q] = 0.f;
+            if (id[q] >= e0 && id[q] < e1) l[q] = p.logits[static_cast<size_t>(t0 + r) * p.E + id[q]];
+        }
+        s = group_sum(s, 8);
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            const int j = sub + 8 * q;
+            if (j >= p.k) continue;
+            pick_id[r][j] = id[q];
+            pick_v[r][j] = w[q] * (dw[q] - s) / (1.f + expf(l[q]));   // 1 - sigmoid(l) = 1 / (1 + exp(l))
+        }
+    }
+
+    // add(token, expert, value) for every expert that a token's picks name
+    template <typename F>
+    __device__ __forceinline__ void add(int k, int e0, int e1, const int32_t (*pick_id)[MOE_MAX_TOPK],
+                                        const float (*pick_v)[MOE_MAX_TOPK], F&& add) const {
+        const int r = threadIdx.x >> 3, sub = threadIdx.x & 7;
+#pragma unroll
+        for (int q = 0; q < N; ++q) {
+            if (id[q] < e0 || id[q] >= e1) continue;
+            // the first pick of an expert adds every pick of it
+            const int j = sub + 8 * q;
+            bool first = true;
+            float sum = pick_v[r][j];
+            for (int i = 0; i < k; ++i) {
+                if (i == j || pick_id[r][i] != id[q]) continue;
+                if (i < j) first = false;
+                else sum += pick_v[r][i];
+            }
+            if (first) add(r, id[q], sum);
+        }
+    }
+};
+
 // Block x + tiles_t y: tokens [32 x, +32), experts [128 y, +128); the blocks
 // behind them split W and an FP32 input into planes. Fragments of a matrix with
 // rows m and summation index c: [m / 32][c / 16][plane][lane], lane l holding
@@ -158,28 +229,8 @@ __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepA
 
     const uint32_t valid = static_cast<uint32_t>(ballot(lane < kPrepRows && t0 + lane < T && p.mask[t0 + lane] != 0));
     if (p.row_bits && by == 0 && tid < 2) p.row_bits[bx * 2 + tid] = valid >> (16 * tid) & 0xFFFFu;
-    // the picks' ids and weights: eight threads a token, up to four picks each
-    const int pr = tid >> 3, sub = tid & 7;
-    constexpr int kPicks = MOE_MAX_TOPK / 8;
-    int id[kPicks];
-    float w[kPicks], dw[kPicks], l[kPicks];
-    if (p.d_topk_w) {
-#pragma unroll
-        for (int q = 0; q < kPicks; ++q) {
-            const int j = sub + 8 * q;
-            const size_t at = static_cast<size_t>(t0 + pr) * k + j;
-            id[q] = -1;
-            w[q] = dw[q] = l[q] = 0.f;
-            if (j < k && (valid >> pr & 1)) {
-                const int e = p.ids[at];
-                if (e >= 0 && e < E) {
-                    id[q] = e;
-                    w[q] = p.topk_w[at];
-                    dw[q] = p.d_topk_w[at];
-                }
-            }
-        }
-    }
+    Picks picks;
+    if (p.d_topk_w) picks.load(p, t0, valid);
     // d_aux: piece i of the tile is row tid / 32 + 8 i, columns 4 (tid % 32) .. +4
     const int col = e0 + 4 * (tid & 31);
     f32x4 v[kPrepLoads];
@@ -195,42 +246,14 @@ __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepA
                     if (col + c < E) v[i][c] = src[c];
         }
     }
-    if (p.d_topk_w) {
-        float s = 0.f;
-#pragma unroll
-        for (int q = 0; q < kPicks; ++q) {
-            s = __builtin_fmaf(w[q], dw[q], s);
-            const bool here = id[q] >= e0 && id[q] < e0 + kPrepCols;
-            if (here) l[q] = p.logits[static_cast<size_t>(t0 + pr) * E + id[q]];
-        }
-        s = group_sum(s, 8);
-#pragma unroll
-        for (int q = 0; q < kPicks; ++q) {
-            const int j = sub + 8 * q;
-            if (j >= k) continue;
-            pick_id[pr][j] = id[q];
-            pick_v[pr][j] = w[q] * (dw[q] - s) / (1.f + expf(l[q]));   // 1 - sigmoid(l) = 1 / (1 + exp(l))
-        }
-    }
+    if (p.d_topk_w) picks.values(p, t0, e0, e0 + kPrepCols, pick_id, pick_v);
 #pragma unroll
     for (int i = 0; i < kPrepLoads; ++i)
         *reinterpret_cast<f32x4*>(&tile[((tid >> 5) + 8 * i) * kPrepStride + 4 * (tid & 31)]) = v[i];
     __syncthreads();
     if (p.d_topk_w) {
-#pragma unroll
-        for (int q = 0; q < kPicks; ++q) {
-            if (id[q] < e0 || id[q] >= e0 + kPrepCols) continue;
-            // the first pick of an expert adds every pick of it
-            const int j = sub + 8 * q;
-            bool first = true;
-            float sum = pick_v[pr][j];
-            for (int i = 0; i < k; ++i) {
-                if (i == j || pick_id[pr][i] != id[q]) continue;
-                if (i < j) first = false;
-                else sum += pick_v[pr][i];
-            }
-            if (first) tile[pr * kPrepStride + id[q] - e0] += sum;
-        }
+        picks.add(k, e0, e0 + kPrepCols, pick_id, pick_v,
+                  [&](int r, int e, float v) { tile[r * kPrepStride + e - e0] += v; });
         __syncthreads();
     }
 #pragma unroll
@@ -271,6 +294,93 @@ __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepA
                 x[j] = tile[(half * kKStep + 8 * (lane >> 5) + j) * kPrepStride + (f >> 1) * 32 + (lane & 31)] * p.scale;
             write_fragment(x, 3, p.frag_w + (mt * ks_n + 2 * bx + half) * 3 * kWave + lane);
         }
+    }
+}
+
+// ---------------------------------------------------------- few tokens ----
+
+constexpr int kFewTokens = 32;
+constexpr int kFewCols = 32;                       // columns of H a block takes
+constexpr int kFewGroups = kPrepBlock / kFewCols;   // groups of threads over the experts
+constexpr int kFewValues = 16384;                  // TP E at most: the gradient of the logits in LDS, 64 KB
+constexpr int kFewExperts = 1024;
+
+// Both products of up to 32 tokens in FP32, without planes, fragments or a
+// workspace, in one launch: a block computes the gradient of the logits itself
+// (in LDS, [expert][token]) and takes 32 columns of H, a thread one column and
+// every eighth expert. It reads W once and writes d_W once, which bounds it;
+// each value of W meets the TP tokens' gradients from LDS. TP: T rounded up.
+template <int TP, bool F32>
+__global__ __launch_bounds__(kPrepBlock) void few_tokens_kernel(const PrepArgs p, const void* __restrict__ hidden,
+                                                               const float* __restrict__ W, void* __restrict__ d_hidden,
+                                                               float* __restrict__ d_W) {
+    extern __shared__ __attribute__((aligned(16))) float grad[];   // [E][TP]
+    __shared__ int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
+    __shared__ float pick_v[kPrepRows][MOE_MAX_TOPK];
+    __shared__ float part[kFewGroups][kFewCols][TP + 1];
+    const int T = p.T, E = p.E, H = p.H;
+    const int tid = threadIdx.x, lane = tid & 63;
+    const uint32_t valid = static_cast<uint32_t>(ballot(lane < T && p.mask[lane] != 0));
+    Picks picks;
+    if (p.d_topk_w) picks.load(p, 0, valid);
+    for (int i = tid; i < E * TP; i += kPrepBlock) {
+        const int t = i / E, e = i - t * E;   // consecutive threads read consecutive experts
+        grad[e * TP + t] = p.d_aux && t < T && (valid >> t & 1) ? p.d_aux[static_cast<size_t>(t) * E + e] : 0.f;
+    }
+    if (p.d_topk_w) picks.values(p, 0, 0, E, pick_id, pick_v);
+    __syncthreads();
+    if (p.d_topk_w) {
+        picks.add(p.k, 0, E, pick_id, pick_v, [&](int t, int e, float v) { grad[e * TP + t] += v; });
+        __syncthreads();
+    }
+    if (p.d_logits && blockIdx.x == 0)
+        for (int i = tid; i < E * T; i += kPrepBlock) {
+            const int t = i / E, e = i - t * E;
+            p.d_logits[i] = grad[e * TP + t];
+        }
+    const int c = tid % kFewCols, group = tid / kFewCols;
+    const int col = static_cast<int>(blockIdx.x) * kFewCols + c;
+    const bool mine = col < H;
+    float h[TP], acc[TP];
+#pragma unroll
+    for (int t = 0; t < TP; ++t) {
+        acc[t] = 0.f;
+        h[t] = 0.f;
+        if (mine && (valid >> t & 1)) {
+            const size_t at = static_cast<size_t>(t) * H + col;
+            if constexpr (F32) h[t] = static_cast<const float*>(hidden)[at];
+            else h[t] = bf16_lo(static_cast<const uint16_t*>(hidden)[at]);
+        }
+    }
+#pragma unroll 4
+    for (int e = group; e < E; e += kFewGroups) {
+        const float w = d_hidden && mine ? W[static_cast<size_t>(e) * H + col] : 0.f;
+        float dw = 0.f;
+#pragma unroll
+        for (int t = 0; t < TP; t += 4) {
+            const f32x4 g = *reinterpret_cast<const f32x4*>(&grad[e * TP + t]);
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                acc[t + i] = __builtin_fmaf(g[i], w, acc[t + i]);
+                dw = __builtin_fmaf(g[i], h[t + i], dw);
+            }
+        }
+        if (d_W && mine) d_W[static_cast<size_t>(e) * H + col] = dw * p.scale;
+    }
+    if (!d_hidden) return;
+#pragma unroll
+    for (int t = 0; t < TP; ++t) part[group][c][t] = acc[t];
+    __syncthreads();
+    for (int i = tid; i < T * kFewCols; i += kPrepBlock) {
+        const int t = i / kFewCols, q = i - t * kFewCols;
+        const int at_col = static_cast<int>(blockIdx.x) * kFewCols + q;
+        if (at_col >= H) continue;
+        float s = part[0][q][t];
+        for (int g = 1; g < kFewGroups; ++g) s += part[g][q][t];
+        s *= p.scale;
+        const size_t at = static_cast<size_t>(t) * H + at_col;
+        if constexpr (F32) static_cast<float*>(d_hidden)[at] = s;
+        else static_cast<uint16_t*>(d_hidden)[at] = static_cast<uint16_t>(f32_to_bf16_rne(s));
     }
 }
 
@@ -590,8 +700,9 @@ __global__ __launch_bounds__(2 * WM * kWave, WM == 4 ? 2 : 1) void product_kerne
 }
 
 // The sum of n partial arrays, in order; zeros without any.
+template <bool BF16_OUT>
 __global__ __launch_bounds__(256) void sum_parts_kernel(const float4* __restrict__ parts, int n, long long quads,
-                                                        float4* __restrict__ out) {
+                                                        void* __restrict__ out) {
     for (long long i = blockIdx.x * 256ll + threadIdx.x; i < quads; i += gridDim.x * 256ll) {
         float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
@@ -602,7 +713,10 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float4* __restrict
             s.z += v.z;
             s.w += v.w;
         }
-        out[i] = s;
+        if constexpr (BF16_OUT)
+            static_cast<u32x2*>(out)[i] = u32x2{cvt_pk_bf16(s.x, s.y), cvt_pk_bf16(s.z, s.w)};
+        else
+            static_cast<float4*>(out)[i] = s;
     }
 }
 
@@ -616,10 +730,11 @@ struct ProductPlan {
 };
 
 // Row tiles of 64, 128 or 256 as the rows need (at most 128 with three planes of
-// each factor, whose operands take twice the registers). K is split where that shortens
-// the product more than the partial sums, written and read once, cost: a step
-// of a 256-row tile is taken as 1 us, partial sums as 4 TB/s.
-inline ProductPlan plan_product(int m, int n, long long k, bool f32, bool may_split) {
+// each factor, whose operands take twice the registers). K is split where that
+// shortens the product more than the partial sums, written and read once, cost:
+// a step is taken as 0.4 us and 0.15 for every 64 rows, a tile's first loads and
+// results as 4 us, partial sums as 4 TB/s and 4 us for their kernel.
+inline ProductPlan plan_product(int m, int n, long long k, bool f32) {
     ProductPlan p;
     p.wm = m <= 64 ? 1 : m <= 128 || f32 ? 2 : 4;
     p.tiles_m = ceil_div(m, 64 * p.wm);
@@ -627,16 +742,15 @@ inline ProductPlan plan_product(int m, int n, long long k, bool f32, bool may_sp
     p.steps = ceil_div(k, kKStep);
     p.nsplit = 1;
     p.split_steps = p.steps;
-    if (!may_split) return p;
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
     const int slots = p.wm == 1 && !f32 ? 512 : 256;   // blocks resident at once
     double best = 0;
-    for (int ns = 1; ns <= 32 && (ns == 1 || p.steps / ns >= 8); ++ns) {
+    for (int ns = 1; ns <= 32 && (ns == 1 || p.steps / ns >= 4); ++ns) {
         const int each = ceil_div(p.steps, ns);
         const int used = ceil_div(p.steps, each);
         const double rounds = static_cast<double>(ceil_div(tiles * used, slots));
-        double us = rounds * each * (0.25 * p.wm);
-        if (used > 1) us += 8e-6 * used * static_cast<double>(m) * n / 4.0;
+        double us = rounds * (each * (0.4 + 0.15 * p.wm) + 4);
+        if (used > 1) us += 4 + 8e-6 * used * static_cast<double>(m) * n / 4.0;
         if (ns == 1 || us < best) {
             best = us;
             p.nsplit = used;
@@ -657,12 +771,22 @@ inline bool route_backward_shape_ok(int T, int H, int E) {
            E <= MOE_MAX_EXPERTS;
 }
 
+// Whether few_tokens_kernel takes the call. Its FP32 work grows with T E H and its
+// threads walk the experts, while the general path's cost is its launches and
+// latency: measured few / general, 16 tokens of 8192 x 256 experts 18 / 31 us, 32
+// of 4096 x 512 43 / 31 (33 tokens), 32 of 8192 x 256 27 / 31, 8 of 1024 x 2560 72
+// / 35, 4 of 8192 x 4096 116 / 113.
+inline bool few_tokens(int T, int E) {
+    const int tp = T <= 4 ? 4 : T <= 8 ? 8 : T <= 16 ? 16 : kFewTokens;
+    return T <= kFewTokens && E <= kFewExperts && tp * E <= (tp < kFewTokens ? kFewValues : kFewValues / 2);
+}
+
 inline RouteBackwardPlan plan_route_backward(int T, int H, int E, int dtype) {
     RouteBackwardPlan p;
     const bool f32 = dtype == MOE_DTYPE_F32;
     p.np_h = f32 ? 3 : 2;
-    p.h = plan_product(T, H, E, f32, false);
-    p.w = plan_product(E, H, T, f32, true);
+    p.h = plan_product(T, H, E, f32);
+    p.w = plan_product(E, H, T, f32);
     const size_t t32 = ceil_div(T, 32), e16 = ceil_div(E, 16), e32 = ceil_div(E, 32);
     size_t at = 0;
     auto take = [&](size_t n) {
@@ -676,7 +800,10 @@ inline RouteBackwardPlan plan_route_backward(int T, int H, int E, int dtype) {
     p.frag_w = take(e32 * t32 * 2 * 3 * kFrag);
     p.w_planes = take(static_cast<size_t>(p.np_h) * E * H * 2);
     p.x_planes = take(f32 ? 3ull * T * H * 2 : 0);
-    p.parts = take(p.w.nsplit > 1 ? sizeof(float) * p.w.nsplit * E * H : 0);
+    // the products run one after the other, so their partial sums share the space
+    const size_t parts_h = p.h.nsplit > 1 ? sizeof(float) * p.h.nsplit * T * H : 0;
+    const size_t parts_w = p.w.nsplit > 1 ? sizeof(float) * p.w.nsplit * E * H : 0;
+    p.parts = take(parts_h > parts_w ? parts_h : parts_w);
     p.bytes = at;
     return p;
 }
@@ -713,7 +840,7 @@ extern "C" size_t moe_route_backward_workspace_bytes(int T, int H, int E, int hi
     using namespace moe;
     if (logits_in || !route_backward_shape_ok(T, H, E)) return 0;
     if (hidden_dtype != MOE_DTYPE_BF16 && hidden_dtype != MOE_DTYPE_F32) return 0;
-    return T == 0 ? 0 : plan_route_backward(T, H, E, hidden_dtype).bytes;
+    return few_tokens(T, E) ? 0 : plan_route_backward(T, H, E, hidden_dtype).bytes;
 }
 
 extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, const void* hidden, int hidden_dtype,
@@ -736,8 +863,8 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         return dim3(static_cast<unsigned>(g < 2048 ? g : 2048));
     };
     if (T == 0)   // no token: the weight's gradient is zero
-        return d_W ? launch(sum_parts_kernel, grid_of(w_quads), dim3(256), 0, stream, nullptr, 0, w_quads,
-                            reinterpret_cast<float4*>(d_W))
+        return d_W ? launch(sum_parts_kernel<false>, grid_of(w_quads), dim3(256), 0, stream, nullptr, 0, w_quads,
+                            static_cast<void*>(d_W))
                    : MOE_OK;
     if (!token_mask || !d_logits || (!d_topk_w && !d_aux)) return MOE_ERR_NULL_ARG;
     if (d_topk_w && (!logits || !topk_ids || !topk_w)) return MOE_ERR_NULL_ARG;
@@ -746,7 +873,8 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
     const bool f32 = hidden_dtype == MOE_DTYPE_F32;
     RouteBackwardPlan p{};
     char* ws = static_cast<char*>(workspace);
-    if (!logits_in) {
+    const bool few = !logits_in && few_tokens(T, E);
+    if (!logits_in && !few) {
         p = plan_route_backward(T, H, E, hidden_dtype);
         if (!workspace || workspace_bytes < p.bytes || (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
             return MOE_ERR_WORKSPACE;
@@ -764,13 +892,35 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
     g.H = H;
     g.scale = scale;
     g.d_logits = d_logits;
+    g.tiles_t = ceil_div(T, kPrepRows);
+    g.tiles_e = ceil_div(E, kPrepCols);
+    const long long grad_blocks = static_cast<long long>(g.tiles_t) * g.tiles_e;
+    if (few && (d_hidden || d_W)) {
+        if (d_aux == d_logits) {
+            // in place: every block below reads all of d_aux, so the gradient
+            // of the logits is written before
+            const int st = launch(logits_gradient_kernel, dim3(static_cast<unsigned>(grad_blocks)), dim3(kPrepBlock), 0,
+                                  stream, g);
+            if (st != MOE_OK) return st;
+            g.d_topk_w = nullptr;
+            g.d_logits = nullptr;
+        }
+        auto run = [&](auto tp) {
+            constexpr int TP = decltype(tp)::value;
+            return launch(f32 ? few_tokens_kernel<TP, true> : few_tokens_kernel<TP, false>,
+                          dim3(ceil_div(H, kFewCols)), dim3(kPrepBlock), sizeof(float) * TP * E, stream, g, hidden, W,
+                          d_hidden, d_W);
+        };
+        return T <= 4    ? run(std::integral_constant<int, 4>())
+               : T <= 8  ? run(std::integral_constant<int, 8>())
+               : T <= 16 ? run(std::integral_constant<int, 16>())
+                         : run(std::integral_constant<int, kFewTokens>());
+    }
     g.frag_h = d_hidden ? reinterpret_cast<u32x4*>(ws + p.frag_h) : nullptr;
     g.np_h = p.np_h;
     g.frag_w = d_W ? reinterpret_cast<u32x4*>(ws + p.frag_w) : nullptr;
     g.row_bits = d_W ? reinterpret_cast<uint32_t*>(ws + p.bits) : nullptr;
-    g.zeros = logits_in ? nullptr : reinterpret_cast<uint32_t*>(ws + p.zeros);
-    g.tiles_t = ceil_div(T, kPrepRows);
-    g.tiles_e = ceil_div(E, kPrepCols);
+    g.zeros = logits_in || few ? nullptr : reinterpret_cast<uint32_t*>(ws + p.zeros);
     auto* w_planes = reinterpret_cast<uint16_t*>(ws + p.w_planes);
     auto* x_planes = reinterpret_cast<uint16_t*>(ws + p.x_planes);
     long long blocks[2] = {0, 0};
@@ -783,7 +933,7 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         blocks[1] = ceil_div(static_cast<long long>(T) * H / 4, kSplitQuads * kPrepBlock);
     }
     g.split_blocks0 = blocks[0];
-    const long long grid = static_cast<long long>(g.tiles_t) * g.tiles_e + blocks[0] + blocks[1];
+    const long long grid = grad_blocks + blocks[0] + blocks[1];
     if (grid >= (1ll << 31)) return MOE_ERR_BAD_SHAPE;
     int st = launch(logits_gradient_kernel, dim3(static_cast<unsigned>(grid)), dim3(kPrepBlock), 0, stream, g);
     if (st != MOE_OK) return st;
@@ -797,9 +947,18 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         a.m = T;
         a.rows = E;
         a.a_steps = ceil_div(E, kKStep);
-        a.c = d_hidden;
-        st = f32 ? launch_product<3, 3, false>(p.h, a, stream) : launch_product<2, 2, true>(p.h, a, stream);
+        const bool split = p.h.nsplit > 1;
+        a.c = split ? static_cast<void*>(ws + p.parts) : d_hidden;
+        st = f32     ? launch_product<3, 3, false>(p.h, a, stream)
+             : split ? launch_product<2, 2, false>(p.h, a, stream)
+                     : launch_product<2, 2, true>(p.h, a, stream);
         if (st != MOE_OK) return st;
+        if (split) {
+            const long long quads = static_cast<long long>(T) * H / 4;
+            st = launch(f32 ? sum_parts_kernel<false> : sum_parts_kernel<true>, grid_of(quads), dim3(256), 0, stream,
+                        reinterpret_cast<const float4*>(ws + p.parts), p.h.nsplit, quads, d_hidden);
+            if (st != MOE_OK) return st;
+        }
     }
     if (d_W) {
         a.a = g.frag_w;
@@ -819,9 +978,8 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         }
         if (st != MOE_OK) return st;
         if (p.w.nsplit > 1)
-            st = launch(sum_parts_kernel, grid_of(w_quads), dim3(256), 0, stream,
-                        reinterpret_cast<const float4*>(ws + p.parts), p.w.nsplit, w_quads,
-                        reinterpret_cast<float4*>(d_W));
+            st = launch(sum_parts_kernel<false>, grid_of(w_quads), dim3(256), 0, stream,
+                        reinterpret_cast<const float4*>(ws + p.parts), p.w.nsplit, w_quads, static_cast<void*>(d_W));
     }
     return st;
 }

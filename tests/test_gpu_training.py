@@ -122,7 +122,7 @@ def _check_balance(g, T, E, k, S, score, spread=1.0, shift=0.0, d_losses=(0.5, 0
 @pytest.mark.parametrize("T,E,k,S", [(1, 1, 1, None), (1, 64, 4, 1), (3, 5, 2, 3), (16, 16, 4, None), (65, 254, 8, 7),
                                      (200, 257, 3, 66), (333, 1001, 8, 5), (130, 2560, 8, 2), (70, 4096, 32, None),
                                      (67, 4095, 2, 3), (2000, 256, 8, 130), (4500, 33, 4, 3), (50, 1500, 5, 2),
-                                     (50, 2000, 5, 2), (50, 700, 5, 2)])
+                                     (50, 2000, 5, 2), (50, 700, 5, 2), (40, 1024, 8, 3), (64, 1023, 8, 60)])
 def test_balance(T, E, k, S, score):
     _check_balance(np.random.default_rng(T * 7 + E), T, E, k, S, score)
 
@@ -349,7 +349,8 @@ def _check_route(g, T, H, E, k, f32, aux=True, weights=True, scale=0.75, dup=Fal
 
 @pytest.mark.parametrize("f32", [False, True])
 @pytest.mark.parametrize("T,H,E,k", [(1, 16, 1, 1), (1, 256, 64, 4), (16, 256, 16, 4), (33, 272, 130, 8),
-                                     (65, 1040, 257, 3), (300, 512, 256, 8), (129, 144, 1000, 32), (1000, 528, 40, 4),
+                                     (65, 1040, 257, 3), (2, 144, 4000, 7), (5, 8192, 392, 29),
+                                     (8, 48, 1000, 32), (31, 528, 500, 11), (32, 2064, 600, 8), (300, 512, 256, 8), (129, 144, 1000, 32), (1000, 528, 40, 4),
                                      (515, 2064, 96, 8)])
 def test_route_backward(T, H, E, k, f32):
     _check_route(np.random.default_rng(T + H + E), T, H, E, k, f32)
@@ -371,12 +372,13 @@ def test_route_backward_repeated_and_dropped_picks():
     _check_route(np.random.default_rng(35), 40, 64, 200, 6, False, dup=True)
 
 
-def test_route_backward_parts_and_in_place():
+@pytest.mark.parametrize("T", [20, 200])
+def test_route_backward_parts_and_in_place(T):
     """Logits-in mode, either gradient alone, and d_logits written over d_aux
     give the same values as the whole call."""
     require_gpu()
     g = np.random.default_rng(36)
-    T, H, E, k = 200, 128, 96, 4
+    H, E, k = 128, 96, 4
     mask = _mask(g, T)
     l, ids = _logits(g, T, E, mask), _ids(g, T, E, k, mask)
     w = np.full((T, k), 1 / k, np.float32)

@@ -117,11 +117,14 @@ def test_route_backward_rejects_before_launch(lib):
     for name in ("dw", "aux", "hidden", "dh", "dW"):
         assert call(**{name: ODD}) == -7, name
     assert call(hidden=None) == -1                        # no input, yet its gradients are wanted
-    need = m.route_backward_workspace_bytes(4, 64, 16, m.MOE_DTYPE_BF16)
+    need = m.route_backward_workspace_bytes(400, 64, 16, m.MOE_DTYPE_BF16)
     assert need % 256 == 0 and need > 0
-    assert call(ws=None) == -4 and call(wsb=need - 1) == -4 and call(ws=V((1 << 20) + 16)) == -4
-    assert m.route_backward_workspace_bytes(4, 64, 16, m.MOE_DTYPE_F32) > need
-    assert m.route_backward_workspace_bytes(4, 64, 16, m.MOE_DTYPE_BF16, logits_in=True) == 0
+    assert call(T=400, ws=None) == -4 and call(T=400, wsb=need - 1) == -4
+    assert call(T=400, ws=V((1 << 20) + 16)) == -4
+    assert m.route_backward_workspace_bytes(400, 64, 16, m.MOE_DTYPE_F32) > need
+    assert m.route_backward_workspace_bytes(400, 64, 16, m.MOE_DTYPE_BF16, logits_in=True) == 0
+    assert m.route_backward_workspace_bytes(4, 64, 16, m.MOE_DTYPE_BF16) == 0     # few tokens: no workspace
+    assert m.route_backward_workspace_bytes(32, 64, 4096, m.MOE_DTYPE_BF16) > 0   # too many experts for that
     assert m.route_backward_workspace_bytes(4, 24, 16, m.MOE_DTYPE_BF16) == 0
     assert call(T=0, dW=None, ws=None) == 0
 
