@@ -28,6 +28,8 @@
  *   - A workspace belongs to one call at a time: two calls that may overlap
  *     (two streams, two captured graphs replayed together) need one each.
  *   - Results are deterministic: every sum has a fixed order.
+ *   - Outputs overlap neither inputs nor each other, except where a call says
+ *     that they may.
  *   - A token is valid when its token_mask byte is nonzero. The logits and
  *     input of other tokens are never inspected (they may hold NaN); their
  *     gradients are zero.
@@ -130,7 +132,7 @@ int moe_balance_loss_backward(const float* d_losses, const float* logits, const 
  * Tokens that take no part have token_loss 0; loss is 0 when n is.
  *
  *   logits [T,E] FP32 (the student's). teacher_ids, teacher_logits [T,K]
- *   int32 / FP32. token_mask [T] u8. temperature finite, > 0.
+ *   int32 / FP32. token_mask [T] u8. 1e-6 <= temperature <= 1e6.
  *   0 <= T <= MOE_MAX_TOKENS, 1 <= E <= MOE_MAX_EXPERTS, 1 <= K <= MOE_MAX_TOPK
  *   (K may exceed E).
  *   loss [1], token_loss [T] FP32, tokens [1] int32: outputs.

@@ -19,8 +19,6 @@
 // results do not depend on timing. A batch of up to kSmallTokens tokens takes
 // one block of sixteen waves instead, which needs no second kernel and no
 // workspace: at such sizes a launch costs more than the work.
-#include <cmath>
-
 #include "launch.hpp"
 #include "scores.hpp"
 
@@ -747,6 +745,9 @@ inline bool distill_shape_ok(int T, int E) {
     return T >= 0 && T <= MOE_MAX_TOKENS && E >= 1 && E <= MOE_MAX_EXPERTS;
 }
 
+// The temperature's square and reciprocal, and logits times it, stay normal.
+inline bool temperature_ok(float t) { return t >= 1e-6f && t <= 1e6f; }
+
 inline bool score_ok(int score) { return score == MOE_SCORE_SIGMOID || score == MOE_SCORE_SOFTMAX; }
 
 }  // namespace
@@ -843,7 +844,7 @@ extern "C" int moe_distill_loss(const float* logits, const int32_t* teacher_ids,
                                 size_t workspace_bytes, void* stream) {
     using namespace moe;
     if (!distill_shape_ok(T, E) || K < 1 || K > MOE_MAX_TOPK) return MOE_ERR_BAD_SHAPE;
-    if (!score_ok(score) || !std::isfinite(temperature) || !(temperature > 0.f)) return MOE_ERR_BAD_ARG;
+    if (!score_ok(score) || !temperature_ok(temperature)) return MOE_ERR_BAD_ARG;
     if (!loss || !tokens) return MOE_ERR_NULL_ARG;
     if (T > 0 && (!logits || !teacher_ids || !teacher_logits || !token_mask || !token_loss)) return MOE_ERR_NULL_ARG;
     if (!all_aligned16(logits, teacher_ids, teacher_logits, token_mask, loss, token_loss, tokens))
@@ -887,7 +888,7 @@ extern "C" int moe_distill_loss_backward(const float* d_loss, const float* logit
                                          int accumulate, float* d_logits, void* stream) {
     using namespace moe;
     if (!distill_shape_ok(T, E) || K < 1 || K > MOE_MAX_TOPK) return MOE_ERR_BAD_SHAPE;
-    if (!score_ok(score) || !std::isfinite(temperature) || !(temperature > 0.f)) return MOE_ERR_BAD_ARG;
+    if (!score_ok(score) || !temperature_ok(temperature)) return MOE_ERR_BAD_ARG;
     if (T == 0) return MOE_OK;
     if (!d_loss || !logits || !teacher_ids || !teacher_logits || !token_mask || !tokens || !d_logits)
         return MOE_ERR_NULL_ARG;

@@ -17,6 +17,11 @@ from . import MOE_DTYPE_BF16, MOE_DTYPE_F32, _BF16, _check, _need, _ptr, _stream
 MOE_SCORE_SIGMOID = 0
 MOE_SCORE_SOFTMAX = 1
 
+try:
+    _current_device = torch._C._cuda_getDevice
+except AttributeError:   # older torch: the public query (slower)
+    _current_device = torch.cuda.current_device
+
 _F32 = (torch.float32,)
 _I32 = (torch.int32,)
 _MASK = (torch.uint8, torch.bool)
@@ -45,6 +50,16 @@ def _scratch(workspace, nbytes, dev):
     elif not workspace.is_cuda or workspace.device != dev or not workspace.is_contiguous():
         raise ValueError("workspace must be a contiguous tensor on %s" % dev)
     return workspace, workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def _call(fn, dev, *args):
+    """The library call on dev and its current stream. The library launches on
+    the current device, so another one is made current for the call."""
+    if dev.index == _current_device():
+        _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
+        return
+    with torch.cuda.device(dev):
+        _check(fn, getattr(lib(), fn)(*args, _stream(dev)))
 
 
 def _table(logits, token_mask):
@@ -104,9 +119,9 @@ def balance_loss(logits: torch.Tensor, topk_ids: torch.Tensor, token_mask: torch
     probs = _out(probs, "probs", torch.float32, (S, E), dev)
     tokens = _out(tokens, "tokens", torch.int32, (S + 2,), dev)
     workspace, ws, ws_len = _scratch(workspace, balance_loss_workspace_bytes(T, E, S), dev)
-    _check("moe_balance_loss", lib().moe_balance_loss(
-        logits.data_ptr(), topk_ids.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), score, T, E, k, S,
-        losses.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(), ws, ws_len, _stream(dev)))
+    _call("moe_balance_loss", dev,
+          logits.data_ptr(), topk_ids.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), score, T, E, k, S,
+          losses.data_ptr(), counts.data_ptr(), probs.data_ptr(), tokens.data_ptr(), ws, ws_len)
     return losses, counts, probs, tokens
 
 
@@ -123,9 +138,9 @@ def balance_loss_backward(d_losses: torch.Tensor, logits: torch.Tensor, token_ma
     _need(counts, "counts", _I32, (S, E), dev)
     _need(tokens, "tokens", _I32, (S + 2,), dev)
     d_logits = _gradient(d_logits, accumulate, T, E, dev)
-    _check("moe_balance_loss_backward", lib().moe_balance_loss_backward(
-        d_losses.data_ptr(), logits.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), counts.data_ptr(),
-        tokens.data_ptr(), score, T, E, k, S, int(bool(accumulate)), d_logits.data_ptr(), _stream(dev)))
+    _call("moe_balance_loss_backward", dev,
+          d_losses.data_ptr(), logits.data_ptr(), token_mask.data_ptr(), _ptr(seq_offsets), counts.data_ptr(),
+          tokens.data_ptr(), score, T, E, k, S, int(bool(accumulate)), d_logits.data_ptr())
     return d_logits
 
 
@@ -154,10 +169,9 @@ def distill_loss(logits: torch.Tensor, teacher_ids: torch.Tensor, teacher_logits
     token_loss = _out(token_loss, "token_loss", torch.float32, (T,), dev)
     tokens = _out(tokens, "tokens", torch.int32, (1,), dev)
     workspace, ws, ws_len = _scratch(workspace, distill_loss_workspace_bytes(T, E), dev)
-    _check("moe_distill_loss", lib().moe_distill_loss(
-        logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(), token_mask.data_ptr(), score,
-        float(temperature), T, E, K, loss.data_ptr(), token_loss.data_ptr(), tokens.data_ptr(), ws, ws_len,
-        _stream(dev)))
+    _call("moe_distill_loss", dev,
+          logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(), token_mask.data_ptr(), score,
+          float(temperature), T, E, K, loss.data_ptr(), token_loss.data_ptr(), tokens.data_ptr(), ws, ws_len)
     return loss, token_loss, tokens
 
 
@@ -172,10 +186,10 @@ def distill_loss_backward(d_loss: torch.Tensor, logits: torch.Tensor, teacher_id
     _scalars(d_loss, "d_loss", 1, _F32, dev)
     _scalars(tokens, "tokens", 1, _I32, dev)
     d_logits = _gradient(d_logits, accumulate, T, E, dev)
-    _check("moe_distill_loss_backward", lib().moe_distill_loss_backward(
-        d_loss.data_ptr(), logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
-        token_mask.data_ptr(), tokens.data_ptr(), score, float(temperature), T, E, K, int(bool(accumulate)),
-        d_logits.data_ptr(), _stream(dev)))
+    _call("moe_distill_loss_backward", dev,
+          d_loss.data_ptr(), logits.data_ptr(), teacher_ids.data_ptr(), teacher_logits.data_ptr(),
+          token_mask.data_ptr(), tokens.data_ptr(), score, float(temperature), T, E, K, int(bool(accumulate)),
+          d_logits.data_ptr())
     return d_logits
 
 
@@ -239,10 +253,9 @@ def route_backward(d_topk_w: Optional[torch.Tensor], hidden: Optional[torch.Tens
     else:
         d_W = None
     workspace, ws, ws_len = _scratch(workspace, route_backward_workspace_bytes(T, H, E, dtype, hidden is None), dev)
-    _check("moe_route_backward", lib().moe_route_backward(
-        _ptr(d_topk_w), _ptr(d_aux), _ptr(hidden), dtype, _ptr(W), _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
-        token_mask.data_ptr(), float(scale), T, H, E, k, d_logits.data_ptr(), _ptr(d_hidden), _ptr(d_W), ws,
-        ws_len, _stream(dev)))
+    _call("moe_route_backward", dev,
+          _ptr(d_topk_w), _ptr(d_aux), _ptr(hidden), dtype, _ptr(W), _ptr(logits), _ptr(topk_ids), _ptr(topk_w),
+          token_mask.data_ptr(), float(scale), T, H, E, k, d_logits.data_ptr(), _ptr(d_hidden), _ptr(d_W), ws, ws_len)
     return d_logits, d_hidden, d_W
 
 
@@ -278,8 +291,8 @@ def combine_backward(d_out: torch.Tensor, expert_out: torch.Tensor, slots: torch
     d_topk_w = _out(d_topk_w, "d_topk_w", torch.float32, (T, k), dev)
     d_norm_w = _out(d_norm_w, "d_norm_w", torch.float32, (H,), dev) if need_norm_w else None
     workspace, ws, ws_len = _scratch(workspace, combine_backward_workspace_bytes(T, R, H), dev)
-    _check("moe_combine_backward", lib().moe_combine_backward(
-        d_out.data_ptr(), expert_out.data_ptr(), R, slots.data_ptr(), topk_w.data_ptr(), norm_w.data_ptr(),
-        float(gain_center), float(eps), T, H, k, d_expert_out.data_ptr(), d_topk_w.data_ptr(), _ptr(d_norm_w), ws,
-        ws_len, _stream(dev)))
+    _call("moe_combine_backward", dev,
+          d_out.data_ptr(), expert_out.data_ptr(), R, slots.data_ptr(), topk_w.data_ptr(), norm_w.data_ptr(),
+          float(gain_center), float(eps), T, H, k, d_expert_out.data_ptr(), d_topk_w.data_ptr(), _ptr(d_norm_w), ws,
+          ws_len)
     return d_expert_out, d_topk_w, d_norm_w

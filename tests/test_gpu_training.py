@@ -122,7 +122,8 @@ def _check_balance(g, T, E, k, S, score, spread=1.0, shift=0.0, d_losses=(0.5, 0
 @pytest.mark.parametrize("T,E,k,S", [(1, 1, 1, None), (1, 64, 4, 1), (3, 5, 2, 3), (16, 16, 4, None), (65, 254, 8, 7),
                                      (200, 257, 3, 66), (333, 1001, 8, 5), (130, 2560, 8, 2), (70, 4096, 32, None),
                                      (67, 4095, 2, 3), (2000, 256, 8, 130), (4500, 33, 4, 3), (50, 1500, 5, 2),
-                                     (50, 2000, 5, 2), (50, 700, 5, 2), (40, 1024, 8, 3), (64, 1023, 8, 60)])
+                                     (50, 2000, 5, 2), (50, 700, 5, 2), (40, 1024, 8, 3), (64, 1023, 8, 60),
+                                     (66000, 9, 2, 4)])
 def test_balance(T, E, k, S, score):
     _check_balance(np.random.default_rng(T * 7 + E), T, E, k, S, score)
 
@@ -268,7 +269,7 @@ def _check_distill(g, T, E, K, score, temperature, edit=None, spread=1.0, shift=
                                                (300, 254, 8, 1.0), (131, 1001, 31, 4.0), (70, 2560, 8, 2.0),
                                                (41, 4096, 32, 1.0), (33, 4093, 5, 0.7), (4200, 40, 3, 1.0),
                                                (9, 5, 12, 1.0), (50, 1500, 5, 2.0), (50, 2000, 5, 1.0),
-                                               (50, 700, 5, 2.0), (50, 400, 5, 2.0)])
+                                               (50, 700, 5, 2.0), (50, 400, 5, 2.0), (132000, 6, 3, 1.0)])
 def test_distill(T, E, K, temperature, score):
     _check_distill(np.random.default_rng(T + E + K), T, E, K, score, temperature)
 
@@ -360,6 +361,13 @@ def test_route_backward_splits_over_tokens():
     """Enough tokens that the weight's gradient is summed in splits."""
     _check_route(np.random.default_rng(31), 5000, 512, 64, 4, False)
     _check_route(np.random.default_rng(32), 3000, 256, 300, 8, True)
+
+
+@pytest.mark.parametrize("T,f32", [(4200, False), (2100, True)])
+def test_route_backward_more_tiles_than_blocks(T, f32):
+    """Blocks of the products that take several tiles, whole ones and the
+    matrix' edges: 17 x 17 of them."""
+    _check_route(np.random.default_rng(37), T, 4112, 40, 4, f32)
 
 
 def test_route_backward_one_source_only():
@@ -455,7 +463,8 @@ def test_combine_backward_widths(H):
 
 
 @pytest.mark.parametrize("T,H,k", [(1, 64, 1), (1, 8192, 8), (2, 1024, 32), (16, 256, 4), (700, 1024, 22),
-                                   (1500, 16, 3), (600, 2304, 2), (530, 4096, 9)])
+                                   (1500, 16, 3), (600, 2304, 2), (530, 4096, 9), (1100, 4104, 3),
+                                   (5000, 520, 2), (70000, 16, 2), (600, 16384, 1)])
 def test_combine_backward_tokens(T, H, k):
     _check_combine(np.random.default_rng(T + H), T, H, k)
 

@@ -76,7 +76,7 @@ def test_distill_loss_rejects_before_launch(lib):
         return lib.moe_distill_loss(logits, ids, z, mask, score, temp, T, E, K, loss, each, tokens, ws, wsb, None)
 
     assert call(T=-1) == -2 and call(E=0) == -2 and call(E=4097) == -2 and call(K=0) == -2 and call(K=33) == -2
-    for temp in (0.0, -1.0, float("inf"), float("nan")):
+    for temp in (0.0, -1.0, 1e-7, 1e7, float("inf"), float("nan")):
         assert call(temp=temp) == -5
     assert call(score=2) == -5
     for name in ("logits", "ids", "z", "mask", "loss", "each", "tokens"):
@@ -145,6 +145,37 @@ def test_combine_backward_rejects_before_launch(lib):
     assert need % 256 == 0 and need > 0
     assert call(ws=None) == -4 and call(wsb=need - 1) == -4
     assert m.combine_backward_workspace_bytes(4, 8, 63) == 0
+
+
+def test_binding_makes_the_tensors_device_current(monkeypatch):
+    """The library launches on the current device: with another one current the
+    call runs inside torch.cuda.device(dev), and its stream is looked up there."""
+    import torch
+    from moe_token_routing_amd import training as tr
+    now, log = [0], []
+
+    class Device:
+        def __init__(self, dev):
+            self.dev = dev
+
+        def __enter__(self):
+            self.was, now[0] = now[0], self.dev.index
+
+        def __exit__(self, *_):
+            now[0] = self.was
+
+    class Lib:
+        def moe_something(self, *args):
+            log.append((now[0], args))
+            return 0
+
+    monkeypatch.setattr(tr, "_current_device", lambda: now[0])
+    monkeypatch.setattr(torch.cuda, "device", Device)
+    monkeypatch.setattr(tr, "_stream", lambda dev: "stream of %d" % dev.index)
+    monkeypatch.setattr(tr, "lib", Lib)
+    tr._call("moe_something", torch.device("cuda", 0), 1, 2)
+    tr._call("moe_something", torch.device("cuda", 3), 4)
+    assert log == [(0, (1, 2, "stream of 0")), (3, (4, "stream of 3"))] and now[0] == 0
 
 
 def test_binding_refuses_cpu_tensors():
