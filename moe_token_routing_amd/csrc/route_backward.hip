@@ -35,6 +35,7 @@ namespace {
 typedef __bf16 bf16x8_t __attribute__((ext_vector_type(8)));
 typedef float f32x16_t __attribute__((ext_vector_type(16)));
 typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+typedef int32_t i32x4 __attribute__((ext_vector_type(4)));
 
 constexpr int kKStep = 16;            // summation index per MFMA
 constexpr int kFrag = 1024;           // bytes of an A fragment: 32 rows x 16
@@ -176,30 +177,31 @@ struct Picks {
 #pragma unroll
         for (int q = 0; q < N; ++q) {
             const int j = sub + 8 * q;
-            if (j >= p.k) continue;
-            pick_id[r][j] = id[q];
+            pick_id[r][j] = id[q];   // -1 from k on
             pick_v[r][j] = w[q] * (dw[q] - s) / (1.f + expf(l[q]));   // 1 - sigmoid(l) = 1 / (1 + exp(l))
         }
     }
 
-    // add(token, expert, value) for every expert that a token's picks name
+    // add(token, expert, value) for every expert that a token's picks name: the
+    // first pick of an expert adds every pick of it, in order
     template <typename F>
-    __device__ __forceinline__ void add(int k, int e0, int e1, const int32_t (*pick_id)[MOE_MAX_TOPK],
+    __device__ __forceinline__ void add(int e0, int e1, const int32_t (*pick_id)[MOE_MAX_TOPK],
                                         const float (*pick_v)[MOE_MAX_TOPK], F&& add) const {
         const int r = threadIdx.x >> 3, sub = threadIdx.x & 7;
+        i32x4 all[MOE_MAX_TOPK / 4];
+#pragma unroll
+        for (int i = 0; i < MOE_MAX_TOPK / 4; ++i) all[i] = *reinterpret_cast<const i32x4*>(&pick_id[r][4 * i]);
 #pragma unroll
         for (int q = 0; q < N; ++q) {
             if (id[q] < e0 || id[q] >= e1) continue;
-            // the first pick of an expert adds every pick of it
             const int j = sub + 8 * q;
-            bool first = true;
+            uint32_t same = 0;
+#pragma unroll
+            for (int i = 0; i < MOE_MAX_TOPK; ++i) same |= static_cast<uint32_t>(all[i / 4][i % 4] == id[q]) << i;
+            if (same & ((1u << j) - 1)) continue;
             float sum = pick_v[r][j];
-            for (int i = 0; i < k; ++i) {
-                if (i == j || pick_id[r][i] != id[q]) continue;
-                if (i < j) first = false;
-                else sum += pick_v[r][i];
-            }
-            if (first) add(r, id[q], sum);
+            for (same &= same - 1; same; same &= same - 1) sum += pick_v[r][__builtin_ctz(same)];
+            add(r, id[q], sum);
         }
     }
 };
@@ -210,7 +212,7 @@ struct Picks {
 // row l % 32, c = 8 (l / 32) .. +8; their values are scaled, d_logits is not.
 // d_aux may be d_logits: a block reads its tile before it writes it.
 __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepArgs p) {
-    const int T = p.T, E = p.E, k = p.k;
+    const int T = p.T, E = p.E;
     const long long grad_blocks = static_cast<long long>(p.tiles_t) * p.tiles_e;
     if (blockIdx.x >= grad_blocks) {
         const long long b = blockIdx.x - grad_blocks;
@@ -219,7 +221,7 @@ __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepA
         return;
     }
     __shared__ __attribute__((aligned(16))) float tile[kPrepRows * kPrepStride];
-    __shared__ int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
+    __shared__ __attribute__((aligned(16))) int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
     __shared__ float pick_v[kPrepRows][MOE_MAX_TOPK];
     const int tid = threadIdx.x, lane = tid & 63;
     const int by = static_cast<int>(blockIdx.x / p.tiles_t), bx = static_cast<int>(blockIdx.x - static_cast<long long>(by) * p.tiles_t);
@@ -252,7 +254,7 @@ __global__ __launch_bounds__(kPrepBlock) void logits_gradient_kernel(const PrepA
         *reinterpret_cast<f32x4*>(&tile[((tid >> 5) + 8 * i) * kPrepStride + 4 * (tid & 31)]) = v[i];
     __syncthreads();
     if (p.d_topk_w) {
-        picks.add(k, e0, e0 + kPrepCols, pick_id, pick_v,
+        picks.add(e0, e0 + kPrepCols, pick_id, pick_v,
                   [&](int r, int e, float v) { tile[r * kPrepStride + e - e0] += v; });
         __syncthreads();
     }
@@ -315,7 +317,7 @@ __global__ __launch_bounds__(kPrepBlock) void few_tokens_kernel(const PrepArgs p
                                                                const float* __restrict__ W, void* __restrict__ d_hidden,
                                                                float* __restrict__ d_W) {
     extern __shared__ __attribute__((aligned(16))) float grad[];   // [E][TP]
-    __shared__ int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
+    __shared__ __attribute__((aligned(16))) int32_t pick_id[kPrepRows][MOE_MAX_TOPK];
     __shared__ float pick_v[kPrepRows][MOE_MAX_TOPK];
     __shared__ float part[kFewGroups][kFewCols][TP + 1];
     const int T = p.T, E = p.E, H = p.H;
@@ -330,7 +332,7 @@ __global__ __launch_bounds__(kPrepBlock) void few_tokens_kernel(const PrepArgs p
     if (p.d_topk_w) picks.values(p, 0, 0, E, pick_id, pick_v);
     __syncthreads();
     if (p.d_topk_w) {
-        picks.add(p.k, 0, E, pick_id, pick_v, [&](int t, int e, float v) { grad[e * TP + t] += v; });
+        picks.add(0, E, pick_id, pick_v, [&](int t, int e, float v) { grad[e * TP + t] += v; });
         __syncthreads();
     }
     if (p.d_logits && blockIdx.x == 0)
@@ -395,7 +397,12 @@ __device__ __forceinline__ void wait_vmcnt() {
 __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xF | (0x3 << 14) | (0x7 << 4)); }
 
 // Block tile 64 WM x 256, 2 WM waves of 64 x 128 (2 x 4 accumulators of
-// v_mfma_f32_32x32x16_bf16).
+// v_mfma_f32_32x32x16_bf16). WM = 4, or 2 with three planes of each factor, whose
+// operands take twice the registers (one wave a SIMD). Batches of fewer rows
+// take the same tile, K split for more blocks: tiles of 64 or 128 rows have too
+// few waves for a CU, two of them on a CU or more stages included (64 tokens of
+// 8192 x 256: 34 us with 256 rows, 35 with 128, 43 with 64; 215 of 2624 x 235:
+// 44, 58 and 60).
 //
 // Pipeline: every K-step's A fragments and B rows go through a ring of SETS LDS
 // stages filled by direct-to-LDS loads of 1 KB, the same number by every wave;
@@ -406,8 +413,9 @@ __device__ __forceinline__ void wait_lgkmcnt0() { __builtin_amdgcn_s_waitcnt(0xF
 // neither kind of load is waited for beside idle matrix cores. Blocks are
 // persistent: the steps of a block's tiles form one sequence, and the loads of
 // the next tile are in flight while the results of the last one are stored.
-template <int NA, int NB, int WM>
+template <int NA, int NB>
 struct ProductShape {
+    static constexpr int WM = NB == 3 ? 2 : 4;
     static constexpr int WAVES = 2 * WM;
     static constexpr int BLOCK = WAVES * kWave;
     static constexpr int BM = 64 * WM, BN = 256;
@@ -445,11 +453,11 @@ struct StepOperands {
     u32x2 b[NB][8];
 };
 
-template <int NA, int NB, int WM, bool BF16_OUT>
-__global__ __launch_bounds__(2 * WM * kWave, WM == 4 ? 2 : 1) void product_kernel(
+template <int NA, int NB, bool BF16_OUT>
+__global__ __launch_bounds__(NB == 3 ? 256 : 512, NB == 3 ? 1 : 2) void product_kernel(
     const ProductArgs p) {
 #ifdef __HIP_DEVICE_COMPILE__   // the host pass only needs the kernel's handle
-    using S = ProductShape<NA, NB, WM>;
+    using S = ProductShape<NA, NB>;
     extern __shared__ __attribute__((aligned(16))) char lds[];
     // The blocks of an XCD (every eighth) take a run of consecutive tiles: row
     // tiles of one column tile first, then column tiles, then K-splits.
@@ -725,32 +733,29 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(const float4* __restrict
 inline size_t round256(size_t b) { return (b + 255) / 256 * 256; }
 
 struct ProductPlan {
-    int wm;   // waves along the rows: block tile 64 wm x 256
     int tiles_m, tiles_n, steps, nsplit, split_steps;
 };
 
-// Row tiles of 64, 128 or 256 as the rows need (at most 128 with three planes of
-// each factor, whose operands take twice the registers). K is split where that
-// shortens the product more than the partial sums, written and read once, cost:
-// a step is taken as 0.4 us and 0.15 for every 64 rows, a tile's first loads and
-// results as 4 us, partial sums as 4 TB/s and 4 us for their kernel.
+// K is split in parts, whose sums a kernel of their own adds up, where a simple
+// model makes that cheaper. Its figures are measured: a step of a block 1.4 us, a
+// tile's first loads and results 5; partial sums read back, and half of their
+// writing, at 4 TB/s, and 4 us for their kernel. It takes 256 CUs whatever the device has, so
+// that the workspace query and the call agree.
 inline ProductPlan plan_product(int m, int n, long long k, bool f32) {
+    constexpr int kBlocks = 256;
     ProductPlan p;
-    p.wm = m <= 64 ? 1 : m <= 128 || f32 ? 2 : 4;
-    p.tiles_m = ceil_div(m, 64 * p.wm);
+    p.tiles_m = ceil_div(m, f32 ? ProductShape<3, 3>::BM : ProductShape<3, 1>::BM);
     p.tiles_n = ceil_div(n, 256);
     p.steps = ceil_div(k, kKStep);
     p.nsplit = 1;
     p.split_steps = p.steps;
     const long long tiles = static_cast<long long>(p.tiles_m) * p.tiles_n;
-    const int slots = p.wm == 1 && !f32 ? 512 : 256;   // blocks resident at once
     double best = 0;
-    for (int ns = 1; ns <= 32 && (ns == 1 || p.steps / ns >= 4); ++ns) {
+    for (int ns = 1; ns <= 32 && (ns == 1 || p.steps / ns >= 2); ++ns) {
         const int each = ceil_div(p.steps, ns);
         const int used = ceil_div(p.steps, each);
-        const double rounds = static_cast<double>(ceil_div(tiles * used, slots));
-        double us = rounds * (each * (0.4 + 0.15 * p.wm) + 4);
-        if (used > 1) us += 4 + 8e-6 * used * static_cast<double>(m) * n / 4.0;
+        double us = static_cast<double>((tiles * used + kBlocks - 1) / kBlocks) * (each * 1.4 + 5);
+        if (used > 1) us += 4 + 6e-6 * used * static_cast<double>(m) * n / 4.0;
         if (ns == 1 || us < best) {
             best = us;
             p.nsplit = used;
@@ -808,29 +813,19 @@ inline RouteBackwardPlan plan_route_backward(int T, int H, int E, int dtype) {
     return p;
 }
 
-template <int NA, int NB, int WM, bool BF16_OUT>
-int launch_product_as(const ProductArgs& a, void* stream) {
-    using S = ProductShape<NA, NB, WM>;
-    const long long total = static_cast<long long>(a.tiles_m) * a.tiles_n * a.nsplit;
-    // one resident grid of persistent blocks, a multiple of the XCDs
-    const int most = device_cu_count() * (2 * S::LDS <= 160 * 1024 ? 2 : 1) / 8 * 8;
-    const long long grid = 8ll * ceil_div(total, 8);
-    return launch(product_kernel<NA, NB, WM, BF16_OUT>, dim3(static_cast<unsigned>(grid < most ? grid : most)),
-                  dim3(S::BLOCK), S::LDS, stream, a);
-}
-
 template <int NA, int NB, bool BF16_OUT>
 int launch_product(const ProductPlan& p, ProductArgs a, void* stream) {
+    using S = ProductShape<NA, NB>;
     a.steps = p.steps;
     a.split_steps = p.split_steps;
     a.tiles_m = p.tiles_m;
     a.tiles_n = p.tiles_n;
     a.nsplit = p.nsplit;
-    if (p.wm == 1) return launch_product_as<NA, NB, 1, BF16_OUT>(a, stream);
-    if constexpr (NB == 3) return launch_product_as<NA, NB, 2, BF16_OUT>(a, stream);
-    else
-        return p.wm == 2 ? launch_product_as<NA, NB, 2, BF16_OUT>(a, stream)
-                         : launch_product_as<NA, NB, 4, BF16_OUT>(a, stream);
+    // one resident grid of persistent blocks, a multiple of the XCDs
+    const long long grid = 8ll * ceil_div(static_cast<long long>(a.tiles_m) * a.tiles_n * a.nsplit, 8);
+    const int most = device_cu_count() / 8 * 8;
+    return launch(product_kernel<NA, NB, BF16_OUT>, dim3(static_cast<unsigned>(grid < most ? grid : most)),
+                  dim3(S::BLOCK), S::LDS, stream, a);
 }
 
 }  // namespace
