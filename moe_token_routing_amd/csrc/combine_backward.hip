@@ -104,6 +104,7 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
         u32x4 y = {0, 0, 0, 0};
         if (tok_ok && mine) y = d_out[t * nvec + tid];
         float acc[8] = {};   // sum over the slots of w rstd x
+        bool named = false;
         for (int j0 = 0; j0 < k; j0 += G) {
             u32x4 x[G];
             float wt[G];
@@ -134,6 +135,7 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
                 a = group_sum(a, tpt);
                 if (tok_ok && j < k && tid == 0 && !ok[g]) d_topk_w[t * k + j] = 0.f;
                 if (!ok[g]) continue;
+                named = true;
                 const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
                 const float ra = rstd * a;
                 if (tid == 0) {
@@ -155,8 +157,9 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
                              &d_rows[static_cast<size_t>(row[g]) * nvec + tid]);
             }
         }
+        if (named)   // the output's gradient of other tokens may hold NaN
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dgain[0][e] = __builtin_fmaf(bf16_at(y, e), acc[e], dgain[0][e]);
+            for (int e = 0; e < 8; ++e) dgain[0][e] = __builtin_fmaf(bf16_at(y, e), acc[e], dgain[0][e]);
     }
     if (part_gain)
         store_gain_part<1, kSmallBlock>(dgain, sub, tid, tpt, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
@@ -326,14 +329,15 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
             d_topk_w[t * k + tid] = ra_of;
             if (pick_r >= 0) owner[pick_r] = static_cast<int32_t>(t * k + tid);
         }
+        if constexpr (SUM) {
+            if (ballot(pick_r >= 0))   // the output's gradient of other tokens may hold NaN
 #pragma unroll
-        for (int i = 0; i < VPT; ++i) {
-            if constexpr (SUM) {
+                for (int i = 0; i < VPT; ++i)
 #pragma unroll
-                for (int e = 0; e < 8; ++e) dgain[i][e] = __builtin_fmaf(bf16_at(y[i], e), acc[i][e], dgain[i][e]);
-            }
-            y[i] = yn[i];
+                    for (int e = 0; e < 8; ++e) dgain[i][e] = __builtin_fmaf(bf16_at(y[i], e), acc[i][e], dgain[i][e]);
         }
+#pragma unroll
+        for (int i = 0; i < VPT; ++i) y[i] = yn[i];
         pick_r = next_r;
         pick_w = next_w;
         load_picks(t + 2 * stride, next_r, next_w);

@@ -479,6 +479,27 @@ def test_combine_backward_rows_named_more_than_once(T, H, k):
     _check_combine(g, T, H, k, slots=np.zeros((T, k), np.int32), R=3, what="one row")
 
 
+@pytest.mark.parametrize("H", [64, 512, 1024, 2048, 4096, 8192])
+def test_combine_backward_tokens_without_a_slot(H):
+    """The output's gradient of tokens whose slots are all invalid is padding:
+    whatever it and their weights hold, nothing of them reaches a result."""
+    require_gpu()
+    note("combine backward, padded tokens, H=%d" % H)
+    g = np.random.default_rng(43 + H)
+    T, k = 13, 3
+    slots = np.arange(T * k, dtype=np.int32).reshape(T, k)
+    slots[::3] = [-1, T * k, -7]
+    x = wl.f32_to_bf16_bits(g.standard_normal((T * k, H)).astype(np.float32))
+    y = wl.f32_to_bf16_bits(g.standard_normal((T, H)).astype(np.float32))
+    w = g.uniform(0.01, 0.5, (T, k)).astype(np.float32)
+    nw = g.uniform(-0.5, 0.5, H).astype(np.float32)
+    want = m.combine_backward(dev(y), dev(x), dev(slots), dev(w), dev(nw), 1.0, 1e-6)
+    y[::3], w[::3] = wl.BF16_NAN, np.inf
+    got = m.combine_backward(dev(y), dev(x), dev(slots), dev(w), dev(nw), 1.0, 1e-6)
+    for a, b in zip(got, want):
+        assert torch.isfinite(b.float()).all() and torch.equal(a, b)
+
+
 def test_combine_backward_zero_sizes():
     require_gpu()
     bf = lambda *s: torch.full(s, float("nan"), dtype=torch.bfloat16, device=DEV)
