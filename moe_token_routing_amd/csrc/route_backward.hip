@@ -379,7 +379,7 @@ __global__ __launch_bounds__(kPrepBlock) void few_tokens_kernel(const PrepArgs p
         if (at_col >= H) continue;
         float s = part[0][q][t];
         for (int g = 1; g < kFewGroups; ++g) s += part[g][q][t];
-        s *= p.scale;
+        s = valid >> t & 1 ? s * p.scale : 0.f;   // W may hold infinities or NaN
         const size_t at = static_cast<size_t>(t) * H + at_col;
         if constexpr (F32) static_cast<float*>(d_hidden)[at] = s;
         else static_cast<uint16_t*>(d_hidden)[at] = static_cast<uint16_t>(f32_to_bf16_rne(s));
@@ -438,6 +438,7 @@ struct ProductArgs {
     const uint16_t* b;         // [NB][rows][n]
     size_t b_plane;            // elements between planes
     const uint32_t* row_bits;  // valid rows of each K-step; NULL: those below `rows`
+    const uint32_t* out_bits;  // valid rows of c, 16 a word: the others get zeros; NULL: all
     const uint16_t* zeros;     // kZeroBytes of zeros
     int m, n, rows, a_steps;   // a_steps: K-steps the fragments hold (>= steps)
     int steps, split_steps;    // K-steps in all, and of one split
@@ -504,9 +505,10 @@ __global__ __launch_bounds__(NB == 3 ? 256 : 512, NB == 3 ? 1 : 2) void product_
             b_src[i] = p.b + (l >> 3) * p.b_plane + row * p.n + n0;
         }
     };
-    // through the constant address space: a scalar load, which the waits for the
+    // through the constant address space: scalar loads, which the waits for the
     // vector loads do not count
-    const auto* bits_at = (const __attribute__((address_space(4))) uint32_t*)(p.row_bits);
+    using scalar_bits = const __attribute__((address_space(4))) uint32_t*;
+    const auto bits_at = (scalar_bits)(p.row_bits), out_at = (scalar_bits)(p.out_bits);
     auto bits_of = [&](int ks) -> uint32_t {
         if (p.row_bits) return bits_at[ks];
         const int left = p.rows - ks * kKStep;
@@ -620,6 +622,21 @@ __global__ __launch_bounds__(NB == 3 ? 256 : 512, NB == 3 ? 1 : 2) void product_
         const int m0 = m_tile * S::BM + wm * 64 + 4 * (lane >> 5);
         const int col = n_tile * S::BN + wn * 128 + 4 * (lane & 31);
         const size_t part = p.nsplit > 1 ? static_cast<size_t>(split) * p.m : 0;
+        if (p.out_bits) {
+            // an invalid row's zeros met B's infinities and NaN, if it has any
+#pragma unroll
+            for (int mi = 0; mi < 2; ++mi) {
+                const int block = min(m_tile * (S::BM / 32) + wm * 2 + mi, m_last);
+                const uint32_t word = out_at[2 * block] | out_at[2 * block + 1] << 16;
+                if (word == ~0u) continue;
+                const uint32_t mine = word >> (4 * (lane >> 5));
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        if (!(mine >> (8 * (i >> 2) + (i & 3)) & 1)) acc[mi][j][i] = 0.f;
+            }
+        }
         auto put = [&](int mi, int i) {
             const int row = m0 + mi * 32 + 8 * (i >> 2) + (i & 3);
             const size_t at = (part + row) * p.n + col;
@@ -914,7 +931,7 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
     g.frag_h = d_hidden ? reinterpret_cast<u32x4*>(ws + p.frag_h) : nullptr;
     g.np_h = p.np_h;
     g.frag_w = d_W ? reinterpret_cast<u32x4*>(ws + p.frag_w) : nullptr;
-    g.row_bits = d_W ? reinterpret_cast<uint32_t*>(ws + p.bits) : nullptr;
+    g.row_bits = logits_in || few ? nullptr : reinterpret_cast<uint32_t*>(ws + p.bits);
     g.zeros = logits_in || few ? nullptr : reinterpret_cast<uint32_t*>(ws + p.zeros);
     auto* w_planes = reinterpret_cast<uint16_t*>(ws + p.w_planes);
     auto* x_planes = reinterpret_cast<uint16_t*>(ws + p.x_planes);
@@ -942,6 +959,7 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         a.m = T;
         a.rows = E;
         a.a_steps = ceil_div(E, kKStep);
+        a.out_bits = g.row_bits;
         const bool split = p.h.nsplit > 1;
         a.c = split ? static_cast<void*>(ws + p.parts) : d_hidden;
         st = f32     ? launch_product<3, 3, false>(p.h, a, stream)
@@ -960,6 +978,7 @@ extern "C" int moe_route_backward(const float* d_topk_w, const float* d_aux, con
         a.m = E;
         a.rows = T;
         a.a_steps = 2 * g.tiles_t;
+        a.out_bits = nullptr;
         a.c = p.w.nsplit > 1 ? static_cast<void*>(ws + p.parts) : static_cast<void*>(d_W);
         if (f32) {   // the planes hold zeros for invalid tokens
             a.b = x_planes;

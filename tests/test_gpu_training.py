@@ -407,6 +407,28 @@ def test_route_backward_parts_and_in_place(T):
         assert torch.equal(a, b)
 
 
+@pytest.mark.parametrize("T,f32", [(7, False), (30, True), (100, False), (300, False), (300, True)])
+def test_route_backward_invalid_rows_beside_a_diverged_weight(T, f32):
+    """Invalid tokens' gradients are zeros whatever the weight holds."""
+    require_gpu()
+    note("route backward, weight with infinities, T=%d" % T)
+    g = np.random.default_rng(36 + T)
+    H, E, k = 272, 40, 3
+    mask = (g.uniform(size=T) >= 0.4).astype(np.uint8)
+    mask[:3] = [0, 1, 0]
+    l, ids = _logits(g, T, E, mask), _ids(g, T, E, k, mask)
+    h = g.standard_normal((T, H)).astype(np.float32)
+    h = h if f32 else wl.f32_to_bf16_bits(h)
+    W = g.standard_normal((E, H)).astype(np.float32)
+    W[4], W[7, ::2] = np.inf, np.nan
+    w = np.full((T, k), 1 / k, np.float32)
+    _, d_h, d_W = m.route_backward(dev(g.standard_normal((T, k)).astype(np.float32)), dev(h), dev(W), dev(l), dev(ids),
+                                   dev(w), dev(mask))
+    d_h = d_h.float().cpu().numpy()
+    assert (d_h[mask == 0] == 0).all() and np.isnan(d_h[mask != 0]).any()
+    assert np.isfinite(host(d_W)).all()
+
+
 def test_route_backward_without_tokens():
     require_gpu()
     e = lambda *s: torch.empty(s, dtype=torch.float32, device=DEV)
