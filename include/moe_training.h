@@ -49,7 +49,8 @@ extern "C" {
  *   MOE_SCORE_SOFTMAX  p = softmax(l)
  * Both are softmax(log score); the sigmoid form is evaluated so that it holds
  * where every s_e underflows. A row whose every score is zero (all logits
- * -inf) has p = 0. */
+ * -inf) has p = 0; it counts as a token, adds nothing to the balance and z
+ * losses and has no gradient of them. */
 enum moe_score {
     MOE_SCORE_SIGMOID = 0,
     MOE_SCORE_SOFTMAX = 1
@@ -129,7 +130,9 @@ int moe_balance_loss_backward(const float* d_losses, const float* logits, const 
  *   token_loss[t] = temperature^2 sum_j q_j (log q_j - log p[id_j])
  *   loss[0]       = 1/n sum_t token_loss[t]
  *   tokens[0]     = n
- * Tokens that take no part have token_loss 0; loss is 0 when n is.
+ * Tokens that take no part have token_loss 0; loss is 0 when n is. An expert
+ * with q > 0 whose student logit is -inf makes the loss infinite; the gradient
+ * is finite there.
  *
  *   logits [T,E] FP32 (the student's). teacher_ids, teacher_logits [T,K]
  *   int32 / FP32. token_mask [T] u8. 1e-6 <= temperature <= 1e6.
@@ -215,7 +218,10 @@ int moe_route_backward(const float* d_topk_w, const float* d_aux, const void* hi
  *   d_expert_out[r,i] = w rstd (g_i d_out[t,i] - x_i rstd^2 A / H)
  *   d_norm_w[i]       = sum_{t,j} w rstd x_i d_out[t,i]
  * A row named by several slots gets the sum of their gradients; a row that no
- * slot names gets zeros and is never read.
+ * slot names gets zeros and is never read. moe_dispatch names every row once,
+ * and the call is made for that: each row named more than once costs a scan of
+ * all slots by one wave. d_out and topk_w of a token whose slots are all
+ * invalid may hold anything.
  *
  *   d_out [T,H] BF16 bits; expert_out [R,H] BF16 bits (may be NULL only if R ==
  *   0); slots [T,k] int32; topk_w [T,k] FP32; norm_w [H] FP32; ranges as in

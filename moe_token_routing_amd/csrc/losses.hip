@@ -155,7 +155,7 @@ __device__ __forceinline__ void balance_part(const Place<WPT, GROUPS>& at, const
             total[1] = u.sum();
         }
         reduce.sum(total);
-        const float lse = m + logf(total[0]);
+        const float lse = total[0] == 0.f ? 0.f : m + logf(total[0]);   // a row of -inf adds nothing
         z += lse * lse;
         const float inv = inverse(total[SIGMOID ? 1 : 0]);
 #pragma unroll
@@ -471,7 +471,7 @@ __global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void balance_bac
             float v[3] = {d.sum(), u.sum(), u.dot(cf)};
             reduce.sum(v);
             // the z loss' part: (2 / n) lse softmax
-            const float zc = zg == 0.f ? 0.f : zg * (m + logf(v[0])) * inverse(v[0]);
+            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + logf(v[0])) * inverse(v[0]);
             const float inv = inverse(v[1]), dot = v[2] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -482,7 +482,7 @@ __global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void balance_bac
             float v[2] = {u.sum(), u.dot(cf)};
             reduce.sum(v);
             const float inv = inverse(v[0]), dot = v[1] * inv;
-            const float zc = zg == 0.f ? 0.f : zg * (m + logf(v[0])) * inv;
+            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + logf(v[0])) * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -617,8 +617,10 @@ __global__ __launch_bounds__(WPT* GROUPS* kWave) void distill_kernel(
             }
             float total[1] = {u.sum()};
             reduce.sum(total);
-            const float lse = m + logf(total[0]);
-            const float term = id >= 0 && q > 0.f ? q * (logq - (log_score(xp, score) - lse)) : 0.f;
+            // an expert that the student masks is infinitely far, in a row of -inf too
+            const float ls = log_score(xp, score);
+            const float logp = ls == kNegInf ? kNegInf : ls - (m + logf(total[0]));
+            const float term = id >= 0 && q > 0.f ? q * (logq - logp) : 0.f;
             loss = temp2 * wave_sum(term);
             sum += loss;
             ++n;

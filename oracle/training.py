@@ -45,8 +45,11 @@ def distribution(l, score):
 
 
 def logsumexp(l):
+    """log sum exp of each row; 0 for a row of -inf, which adds nothing."""
     top = l.max(axis=1, keepdims=True)
-    return (top + np.log(np.exp(l - top).sum(axis=1, keepdims=True)))[:, 0]
+    top = np.where(top == -np.inf, 0.0, top)
+    total = np.exp(l - top).sum(axis=1, keepdims=True)
+    return np.where(total > 0, top + np.log(np.where(total > 0, total, 1.0)), 0.0)[:, 0]
 
 
 def _members(mask, seq_offsets, T):

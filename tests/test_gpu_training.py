@@ -169,6 +169,42 @@ def test_balance_masked_experts(score):
     assert np.isfinite(host(probs)).all() and np.isfinite(host(losses)[0])
 
 
+@pytest.mark.parametrize("score", [OT.SIGMOID, OT.SOFTMAX])
+@pytest.mark.parametrize("T,E", [(30, 40), (90, 300), (70, 1500)])
+def test_losses_of_rows_without_an_expert(T, E, score):
+    """Rows whose every logit is -inf: p = 0, nothing in the balance and z
+    losses and no gradient of them; the distillation loss is infinite there,
+    its gradient finite."""
+    require_gpu()
+    note("losses, rows of -inf, T=%d E=%d" % (T, E))
+    g = np.random.default_rng(16)
+    k = 4
+    mask = np.ones(T, np.uint8)
+    l = g.standard_normal((T, E)).astype(np.float32)
+    l[5:T:7] = -np.inf
+    ids = _ids(g, T, E, k, mask)
+    off = np.array([0, 5, 6, T], np.int32)   # the second sequence has such a row alone
+    ref = OT.balance_loss(l, ids, mask, off, score)
+    losses, counts, probs, tokens = m.balance_loss(dev(l), dev(ids), dev(mask), score=score, seq_offsets=dev(off))
+    P = _prob_tol(l, mask, E)
+    _close(host(probs), ref[2], (P + 40 * U) * ref[2], "probs")
+    lse = np.sqrt(ref[0][1])
+    _close(host(losses), ref[0], [(P + 56 * U) * ref[0][0], 2 * (lse + 1) * (P + 4 * U * (lse + 1)) + 40 * U * ref[0][1]],
+           "losses")
+    gl = np.array([1.0, 1.0], np.float32)
+    d = host(m.balance_loss_backward(dev(gl), dev(l), dev(mask), counts, tokens, k, score=score, seq_offsets=dev(off)))
+    want, mag = OT.balance_loss_backward(gl, l, mask, ref[1], ref[3], k, off, score)
+    _close(d, want, 4 * P * mag, "d_logits")
+    assert (d[5:T:7] == 0).all()
+    z = g.standard_normal((T, k)).astype(np.float32)
+    loss, each, n = m.distill_loss(dev(l), dev(ids), dev(z), dev(mask), score=score)
+    assert np.isposinf(host(each)[5:T:7]).all() and np.isposinf(host(loss)[0]) and int(host(n)[0]) == T
+    assert np.isfinite(np.delete(host(each), np.arange(5, T, 7))).all()
+    d = host(m.distill_loss_backward(dev(np.ones(1, np.float32)), dev(l), dev(ids), dev(z), dev(mask), n, score=score))
+    want, mag = OT.distill_loss_backward(1.0, l, ids, z, mask, T, score)
+    _close(d, want, 3 * (P + _prob_tol(z, mask, E)) * mag + 1e-37, "distillation d_logits")
+
+
 def test_balance_without_tokens():
     require_gpu()
     E, S = 24, 3
