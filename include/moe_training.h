@@ -135,7 +135,8 @@ int moe_balance_loss_backward(const float* d_losses, const float* logits, const 
  * is finite there.
  *
  *   logits [T,E] FP32 (the student's). teacher_ids, teacher_logits [T,K]
- *   int32 / FP32. token_mask [T] u8. 1e-6 <= temperature <= 1e6.
+ *   int32 / FP32. token_mask [T] u8. 1e-6 <= temperature <= 1e6; a quotient
+ *   outside FP32's range counts as infinite.
  *   0 <= T <= MOE_MAX_TOKENS, 1 <= E <= MOE_MAX_EXPERTS, 1 <= K <= MOE_MAX_TOPK
  *   (K may exceed E).
  *   loss [1], token_loss [T] FP32, tokens [1] int32: outputs.

@@ -676,6 +676,103 @@ def test_training_step_replayed_from_a_graph_on_a_side_stream():
         assert torch.equal(again["d_W"], eager[i]["d_W"])
 
 
+def test_training_steps_on_two_streams_at_once():
+    """Two chains in flight together, each with its own inputs and buffers."""
+    require_gpu()
+    note("training steps on two streams")
+    g = np.random.default_rng(54)
+    k, E = 4, 96
+    sets = [{n: dev(v) for n, v in _step_inputs(g, T, H, E, k, _mask(g, T)).items()} for T, H in ((260, 512), (700, 1024))]
+    off = dev(np.array([0, 90, 250], np.int32))
+    gl, gd = torch.tensor([0.02, 0.001], device=DEV), torch.tensor([0.1], device=DEV)
+    alone = [_step(s, k, E, off, gl, gd) for s in sets]
+    streams = [torch.cuda.Stream() for _ in sets]
+    torch.cuda.synchronize()
+    got = [[], []]
+    for _ in range(4):
+        for i, stream in enumerate(streams):
+            with torch.cuda.stream(stream):
+                got[i].append(_step(sets[i], k, E, off, gl, gd))
+    torch.cuda.synchronize()
+    for i, want in enumerate(alone):
+        for r in got[i]:
+            for n, b in want.items():
+                a, b = (t.nan_to_num(7.0) if t.is_floating_point() else t for t in (r[n], b))
+                assert torch.equal(a, b), n
+
+
+def test_tables_of_more_than_2_32_elements():
+    """Long batches and large expert tables, of which only the end is valid,
+    against the same work on that end alone."""
+    require_gpu()
+    T, E, k, H, n = (1 << 20) + 640, 4096, 2, 16, 320
+    note("tables of more than 2^32 elements")
+    torch.manual_seed(55)
+    g = np.random.default_rng(55)
+    l = torch.empty((T, E), device=DEV).normal_()
+    mask = torch.zeros(T, dtype=torch.uint8, device=DEV)
+    tail = _mask(g, n)
+    mask[-n:] = dev(tail)
+    ids = torch.randint(0, E // k, (T, k), dtype=torch.int32, device=DEV)
+    ids[:, 1] += E // k
+    assert l.numel() - n * E > 1 << 32
+    end = [t[-n:].clone() for t in (l, ids, mask)]
+    # balance: the same rows in the same order; sums of up to n tokens
+    whole, part = m.balance_loss(l, ids, mask), m.balance_loss(*end)
+    assert torch.equal(whole[1], part[1]) and torch.equal(whole[3], part[3])
+    p = host(part[2]).astype(np.float64)
+    _close(host(whole[2]), p, 2 * n * U * p, "probs")
+    b = host(part[0]).astype(np.float64)
+    _close(host(whole[0]), b, 4 * n * U * b, "losses")
+    gl = torch.ones(2, device=DEV)
+    d = m.balance_loss_backward(gl, l, mask, whole[1], whole[3], k)
+    assert torch.equal(d[-n:], m.balance_loss_backward(gl, end[0], end[2], part[1], part[3], k))
+    assert int(torch.count_nonzero(d[:-n])) == 0
+    # distillation
+    z = torch.empty((T, k), device=DEV).normal_()
+    whole, part = m.distill_loss(l, ids, z, mask), m.distill_loss(end[0], end[1], z[-n:], end[2])
+    assert torch.equal(whole[1][-n:], part[1]) and torch.equal(whole[2], part[2])
+    assert int(torch.count_nonzero(whole[1][:-n])) == 0
+    b = abs(float(part[0])) + float(part[1].abs().sum()) / n
+    assert abs(float(whole[0]) - float(part[0])) <= 2 * n * U * b
+    d = m.distill_loss_backward(gl[:1], l, ids, z, mask, whole[2], d_logits=d)
+    assert torch.equal(d[-n:], m.distill_loss_backward(gl[:1], end[0], end[1], z[-n:], end[2], part[2]))
+    assert int(torch.count_nonzero(d[:-n])) == 0
+    # route
+    w = torch.full((T, k), 0.5, device=DEV)
+    h = g.standard_normal((n, H)).astype(np.float32)
+    h = wl.f32_to_bf16_bits(h)
+    W = g.standard_normal((E, H)).astype(np.float32)
+    hidden = torch.full((T, H), float("nan"), dtype=torch.bfloat16, device=DEV)
+    hidden[-n:] = dev(h)
+    d, d_h, d_W = m.route_backward(z, hidden, dev(W), l, ids, w, mask, d_logits=d)
+    (wl_, wh, wW), (ml, mh, mW) = OT.route_backward(host(z[-n:]), h, W, host(end[0]), host(end[1]),
+                                                   np.full((n, k), 0.5, np.float32), tail)
+    _close(host(d[-n:]), wl_, 40 * U * ml, "d_logits")
+    _close(host(d_h[-n:]), wh, ((6 * E / 16 + 64) * U + 3 * 2.0 ** -17) * mh + 2.0 ** -8 * np.abs(wh), "d_hidden")
+    # zeros add without a rounding: n tokens' steps count, and the splits
+    _close(host(d_W), wW, (40 + 6 * (n / 16 + 1) + 64 + 3) * U * mW, "d_W")
+    assert int(torch.count_nonzero(d[:-n])) == 0 and int(torch.count_nonzero(d_h[:-n])) == 0
+    del l, d, d_h, z, w, hidden
+    # combine
+    T, H, R, k = 64, 8192, (1 << 19) + 100, 3
+    slots = torch.randperm(R, device=DEV)[:T * k].to(torch.int32)
+    slots[:4] = torch.tensor([R - 1, 0, R - 2, 1 << 19], dtype=torch.int32)
+    slots = slots.unique()   # ascending
+    slots = slots[torch.randperm(len(slots), device=DEV)][:T * k - 6].view(-1, k).contiguous()
+    T = slots.shape[0]
+    x = torch.empty((R, H), dtype=torch.bfloat16, device=DEV)
+    x.fill_(float("nan"))
+    rows = slots.flatten().long()
+    x[rows] = torch.randn((T * k, H), device=DEV).bfloat16()
+    y, tw, nw = torch.randn((T, H), device=DEV).bfloat16(), torch.rand((T, k), device=DEV), torch.rand(H, device=DEV)
+    got = m.combine_backward(y, x, slots, tw, nw, 1.0, 1e-6)
+    small = torch.arange(T * k, dtype=torch.int32, device=DEV).view(T, k)
+    want = m.combine_backward(y, x[rows], small, tw, nw, 1.0, 1e-6)
+    assert torch.equal(got[0][rows], want[0]) and torch.equal(got[1], want[1]) and torch.equal(got[2], want[2])
+    assert int(torch.count_nonzero(got[0])) == int(torch.count_nonzero(want[0]))
+
+
 def test_workspace_left_by_a_larger_call():
     """A call that is given a workspace full of another call's values, or of
     NaN, gives the same results: nothing is read before it is written."""
