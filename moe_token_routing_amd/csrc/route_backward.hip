@@ -439,6 +439,7 @@ struct ProductArgs {
     size_t b_plane;            // elements between planes
     const uint32_t* row_bits;  // valid rows of each K-step; NULL: those below `rows`
     const uint32_t* out_bits;  // valid rows of c, 16 a word: the others get zeros; NULL: all
+                               // (as many planes of each factor: the input's gradient)
     const uint16_t* zeros;     // kZeroBytes of zeros
     int m, n, rows, a_steps;   // a_steps: K-steps the fragments hold (>= steps)
     int steps, split_steps;    // K-steps in all, and of one split
@@ -622,28 +623,27 @@ __global__ __launch_bounds__(NB == 3 ? 256 : 512, NB == 3 ? 1 : 2) void product_
         const int m0 = m_tile * S::BM + wm * 64 + 4 * (lane >> 5);
         const int col = n_tile * S::BN + wn * 128 + 4 * (lane & 31);
         const size_t part = p.nsplit > 1 ? static_cast<size_t>(split) * p.m : 0;
-        if (p.out_bits) {
-            // an invalid row's zeros met B's infinities and NaN, if it has any
+        // an invalid row's zeros met B's infinities and NaN, if it has any
+        uint32_t valid[2] = {~0u, ~0u};
+        if (NA == NB && p.out_bits) {
 #pragma unroll
             for (int mi = 0; mi < 2; ++mi) {
                 const int block = min(m_tile * (S::BM / 32) + wm * 2 + mi, m_last);
-                const uint32_t word = out_at[2 * block] | out_at[2 * block + 1] << 16;
-                if (word == ~0u) continue;
-                const uint32_t mine = word >> (4 * (lane >> 5));
-#pragma unroll
-                for (int i = 0; i < 16; ++i)
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-                        if (!(mine >> (8 * (i >> 2) + (i & 3)) & 1)) acc[mi][j][i] = 0.f;
+                valid[mi] = (out_at[2 * block] | out_at[2 * block + 1] << 16) >> (4 * (lane >> 5));
             }
         }
         auto put = [&](int mi, int i) {
             const int row = m0 + mi * 32 + 8 * (i >> 2) + (i & 3);
             const size_t at = (part + row) * p.n + col;
             const float v0 = acc[mi][0][i], v1 = acc[mi][1][i], v2 = acc[mi][2][i], v3 = acc[mi][3][i];
+            const uint32_t keep = -(valid[mi] >> (8 * (i >> 2) + (i & 3)) & 1u);
             if constexpr (BF16_OUT)
                 *reinterpret_cast<u32x2*>(static_cast<uint16_t*>(p.c) + at) =
-                    u32x2{cvt_pk_bf16(v0, v1), cvt_pk_bf16(v2, v3)};
+                    u32x2{cvt_pk_bf16(v0, v1) & keep, cvt_pk_bf16(v2, v3) & keep};
+            else if constexpr (NA == NB)
+                *reinterpret_cast<u32x4*>(static_cast<float*>(p.c) + at) =
+                    u32x4{__float_as_uint(v0) & keep, __float_as_uint(v1) & keep, __float_as_uint(v2) & keep,
+                          __float_as_uint(v3) & keep};
             else
                 *reinterpret_cast<float4*>(static_cast<float*>(p.c) + at) = make_float4(v0, v1, v2, v3);
         };
