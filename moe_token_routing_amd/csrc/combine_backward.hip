@@ -422,10 +422,9 @@ __device__ __forceinline__ void reduce_gain(const float* __restrict__ part, int 
     const int col = threadIdx.x % kGainCols, group = threadIdx.x / kGainCols;
     const int c = b * kGainCols + col;
     float v = 0.f;
-    if (c < H) {
-#pragma unroll 16
-        for (int r = group; r < rows; r += kGainGroups) v += part[static_cast<size_t>(r) * H + c];
-    }
+    if (c < H)
+        for_batches<16>(group, rows, kGainGroups, [&](int r) { return part[static_cast<size_t>(r) * H + c]; },
+                        [&](float p) { v += p; });
     s[group][col] = v;
     __syncthreads();
     if (group == 0 && c < H) {

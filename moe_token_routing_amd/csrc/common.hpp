@@ -106,6 +106,21 @@ __device__ __forceinline__ uint64_t lanemask_lt() {
     return lane == 0 ? 0ull : (~0ull >> (64 - lane));
 }
 
+// add(load(i)) for i = first, first + step, .. below end, in order, N loads at a
+// time in flight; those from end on repeat the last one and are dropped (a plain
+// unrolled loop takes what is left of N one by one).
+template <int N, typename Load, typename Add>
+__device__ __forceinline__ void for_batches(int first, int end, int step, Load&& load, Add&& add) {
+    for (int i = first; i < end; i += N * step) {
+        decltype(load(i)) v[N];
+#pragma unroll
+        for (int n = 0; n < N; ++n) v[n] = load(min(i + n * step, end - 1));
+#pragma unroll
+        for (int n = 0; n < N; ++n)
+            if (i + n * step < end) add(v[n]);
+    }
+}
+
 inline int ceil_div(long long a, long long b) { return (int)((a + b - 1) / b); }
 
 // NULL counts as aligned; NULL checks are separate.

@@ -295,6 +295,11 @@ __global__ __launch_bounds__(kSmallGroups* kWave) void balance_small_kernel(
 
 constexpr int kReduceBlock = 1024;
 
+struct PartSum {
+    float f;
+    int32_t n;
+};
+
 template <typename V>
 __device__ __forceinline__ V agent_load(const V* p) {
     return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
@@ -334,25 +339,27 @@ __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
     const int b0 = a / chunk, b1 = a < b ? (b - 1) / chunk + 1 : b0;
     float p = 0.f;
     int32_t n = 0;
-    if (c < E) {
-#pragma unroll 8
-        for (int r = b0 + group; r < b1; r += kReduceGroups) {
-            const size_t at = (static_cast<size_t>(r) + s) * E + c;
-            p += part_probs[at];
-            n += part_counts[at];
-        }
-    }
+    if (c < E)
+        for_batches<8>(b0 + group, b1, kReduceGroups,
+                       [&](int r) {
+                           const size_t at = (static_cast<size_t>(r) + s) * E + c;
+                           return PartSum{part_probs[at], part_counts[at]};
+                       },
+                       [&](const PartSum& v) {
+                           p += v.f;
+                           n += v.n;
+                       });
     sp[group][col] = p;
     sc[group][col] = n;
     if (threadIdx.x >= kReduceBlock - kWave && cb == 0) {
         int32_t m = 0;
         float z = 0.f;
         const int i = threadIdx.x - (kReduceBlock - kWave);
-#pragma unroll 8
-        for (int r = b0 + i; r < b1; r += kWave) {
-            m += part_n[r + s];
-            z += part_z[r + s];
-        }
+        for_batches<8>(b0 + i, b1, kWave, [&](int r) { return PartSum{part_z[r + s], part_n[r + s]}; },
+                       [&](const PartSum& v) {
+                           m += v.n;
+                           z += v.f;
+                       });
         z = wave_sum(z);
         for (int off = 32; off >= 1; off >>= 1) m += __shfl_xor(m, off, kWave);
         if (i == 0) {
@@ -654,11 +661,11 @@ __global__ __launch_bounds__(kDistillReduceBlock) void distill_reduce_kernel(con
                                                                              int32_t* __restrict__ tokens) {
     __shared__ double red[kDistillReduceBlock / kWave * 2];
     double v[2] = {0, 0};
-#pragma unroll 4
-    for (int b = threadIdx.x; b < blocks; b += kDistillReduceBlock) {
-        v[0] += part_loss[b];
-        v[1] += part_n[b];
-    }
+    for_batches<8>(threadIdx.x, blocks, kDistillReduceBlock, [&](int b) { return PartSum{part_loss[b], part_n[b]}; },
+                   [&](const PartSum& p) {
+                       v[0] += p.f;
+                       v[1] += p.n;
+                   });
     block_sum(v, red);
     if (threadIdx.x == 0) {
         loss[0] = v[1] > 0 ? static_cast<float>(v[0] / v[1]) : 0.f;
