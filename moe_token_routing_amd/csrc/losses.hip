@@ -104,23 +104,29 @@ __device__ __forceinline__ void for_rows(uint64_t bits, const float* __restrict_
 // 1 / total, or 0 for a row whose every weight is zero.
 __device__ __forceinline__ float inverse(float total) { return total == 0.f ? 0.f : 1.f / total; }
 
-// Block sum of N doubles per thread, in a fixed order; thread 0 gets it.
-template <int N>
+// Block sum of N doubles per thread, in a fixed order; the first wave gets it.
+// The waves' sums meet in one wave's lanes: added up by a thread in turn they
+// took 3 us of the sixteen waves' reductions.
+template <int N, int BLOCK>
 __device__ __forceinline__ void block_sum(double (&v)[N], double* red) {
+    constexpr int WAVES = BLOCK / kWave;
+    static_assert(WAVES * N <= kWave && (WAVES & (WAVES - 1)) == 0 && (N & (N - 1)) == 0, "one wave's lanes");
 #pragma unroll
-    for (int i = 0; i < N; ++i)
-        for (int off = 32; off >= 1; off >>= 1) v[i] += __shfl_xor(v[i], off, kWave);
-    const int wave = threadIdx.x / kWave, waves = blockDim.x / kWave;
+    for (int off = 32; off >= 1; off >>= 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], off, kWave);
+    const int wave = threadIdx.x / kWave;
     if (__lane_id() == 0)
 #pragma unroll
         for (int i = 0; i < N; ++i) red[wave * N + i] = v[i];
     __syncthreads();
-    if (threadIdx.x == 0)
+    if (wave == 0) {
+        double s = red[__lane_id() % (WAVES * N)];
 #pragma unroll
-        for (int i = 0; i < N; ++i) {
-            v[i] = red[i];
-            for (int w = 1; w < waves; ++w) v[i] += red[w * N + i];
-        }
+        for (int off = N; off < WAVES * N; off <<= 1) s += __shfl_xor(s, off, kWave);
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] = __shfl(s, i, kWave);
+    }
     __syncthreads();
 }
 
@@ -271,7 +277,7 @@ __global__ __launch_bounds__(kSmallGroups* kWave) void balance_small_kernel(
                 h = hist[c];
             }
             double v[1] = {static_cast<double>(p * static_cast<float>(h))};
-            block_sum(v, red);
+            block_sum<1, P::BLOCK>(v, red);
             if (c == 0) {
                 balance += v[0] * E / (static_cast<double>(k) * m * m);
                 for (int w = 0; w < kSmallGroups; ++w) z += zs[w];
@@ -414,7 +420,7 @@ __global__ __launch_bounds__(kReduceBlock) void balance_reduce_kernel(
         v[2] += m;
         v[3] += m > 0;
     }
-    block_sum(v, red);
+    block_sum<4, kReduceBlock>(v, red);
     if (threadIdx.x == 0) {
         losses[0] = v[3] > 0 ? static_cast<float>(v[0] / v[3]) : 0.f;
         losses[1] = v[2] > 0 ? static_cast<float>(v[1] / v[2]) : 0.f;
@@ -666,7 +672,7 @@ __global__ __launch_bounds__(kDistillReduceBlock) void distill_reduce_kernel(con
                        v[0] += p.f;
                        v[1] += p.n;
                    });
-    block_sum(v, red);
+    block_sum<2, kDistillReduceBlock>(v, red);
     if (threadIdx.x == 0) {
         loss[0] = v[1] > 0 ? static_cast<float>(v[0] / v[1]) : 0.f;
         tokens[0] = static_cast<int32_t>(v[1]);
