@@ -104,6 +104,34 @@ __device__ __forceinline__ void for_rows(uint64_t bits, const float* __restrict_
 // 1 / total, or 0 for a row whose every weight is zero.
 __device__ __forceinline__ float inverse(float total) { return total == 0.f ? 0.f : 1.f / total; }
 
+// Sum of a double over the wave by register exchanges alone: within fours, the
+// mirrored halves of eights and sixteens, then rows of 16 and 32 lanes (64-bit
+// shuffles go through LDS, two a step).
+template <int CTRL>
+__device__ __forceinline__ double dpp_f64(double v) {
+    const uint64_t b = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __builtin_amdgcn_update_dpp(0, static_cast<int>(b), CTRL, 0xF, 0xF, false);
+    const uint32_t hi = __builtin_amdgcn_update_dpp(0, static_cast<int>(b >> 32), CTRL, 0xF, 0xF, false);
+    return __builtin_bit_cast(double, static_cast<uint64_t>(hi) << 32 | lo);
+}
+__device__ __forceinline__ double wave_sum_f64(double v) {
+    v += dpp_f64<0xB1>(v);    // quad_perm [1,0,3,2]
+    v += dpp_f64<0x4E>(v);    // quad_perm [2,3,0,1]
+    v += dpp_f64<0x141>(v);   // row_half_mirror
+    v += dpp_f64<0x140>(v);   // row_mirror
+    auto halves = [](const auto& lo, const auto& hi) {
+        return __builtin_bit_cast(double, static_cast<uint64_t>(hi[0]) << 32 | lo[0]) +
+               __builtin_bit_cast(double, static_cast<uint64_t>(hi[1]) << 32 | lo[1]);
+    };
+    uint64_t b = __builtin_bit_cast(uint64_t, v);
+    uint32_t lo = static_cast<uint32_t>(b), hi = static_cast<uint32_t>(b >> 32);
+    v = halves(__builtin_amdgcn_permlane16_swap(lo, lo, false, false), __builtin_amdgcn_permlane16_swap(hi, hi, false, false));
+    b = __builtin_bit_cast(uint64_t, v);
+    lo = static_cast<uint32_t>(b);
+    hi = static_cast<uint32_t>(b >> 32);
+    return halves(__builtin_amdgcn_permlane32_swap(lo, lo, false, false), __builtin_amdgcn_permlane32_swap(hi, hi, false, false));
+}
+
 // Block sum of N doubles per thread, in a fixed order; the first wave gets it.
 // The waves' sums meet in one wave's lanes: added up by a thread in turn they
 // took 3 us of the sixteen waves' reductions.
@@ -112,9 +140,7 @@ __device__ __forceinline__ void block_sum(double (&v)[N], double* red) {
     constexpr int WAVES = BLOCK / kWave;
     static_assert(WAVES * N <= kWave && (WAVES & (WAVES - 1)) == 0 && (N & (N - 1)) == 0, "one wave's lanes");
 #pragma unroll
-    for (int off = 32; off >= 1; off >>= 1)
-#pragma unroll
-        for (int i = 0; i < N; ++i) v[i] += __shfl_xor(v[i], off, kWave);
+    for (int i = 0; i < N; ++i) v[i] = wave_sum_f64(v[i]);
     const int wave = threadIdx.x / kWave;
     if (__lane_id() == 0)
 #pragma unroll
