@@ -76,6 +76,36 @@ __device__ __forceinline__ void store_gain_part(const float (&dgain)[VPT][8], in
     }
 }
 
+// Sums of N values over aligned groups of `width` lanes (a power of two) by
+// register exchanges alone, the N interleaved: within fours, the mirrored halves
+// of eights and sixteens, then rows of 16 lanes.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+    return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xF, 0xF, false));
+}
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], int width) {
+    if (width > 1)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += dpp_f32<0xB1>(v[i]);    // quad_perm [1,0,3,2]
+    if (width > 2)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += dpp_f32<0x4E>(v[i]);    // quad_perm [2,3,0,1]
+    if (width > 4)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += dpp_f32<0x141>(v[i]);   // row_half_mirror
+    if (width > 8)
+#pragma unroll
+        for (int i = 0; i < N; ++i) v[i] += dpp_f32<0x140>(v[i]);   // row_mirror
+    if (width > 16)
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            const uint32_t u = __float_as_uint(v[i]);
+            const auto s = __builtin_amdgcn_permlane16_swap(u, u, false, false);
+            v[i] = __uint_as_float(s[0]) + __uint_as_float(s[1]);
+        }
+}
+
 // Rows of up to 32 vectors: tpt threads per token (a power of two), one vector
 // each, several tokens in a wave.
 __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
@@ -123,16 +153,22 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
                 x[g] = u32x4{0, 0, 0, 0};
                 if (ok[g] && mine) x[g] = load_nt(&expert_out[static_cast<size_t>(row[g]) * nvec + tid]);
             }
+            float sums[2 * G];
 #pragma unroll
             for (int g = 0; g < G; ++g) {
-                const int j = j0 + g;
                 float ss = 0.f, a = 0.f;
 #pragma unroll
                 for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][q], ss);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) a = __builtin_fmaf(bf16_at(x[g], e), bf16_at(y, e) * gain[e], a);
-                ss = group_sum(ss, tpt);
-                a = group_sum(a, tpt);
+                sums[2 * g] = ss;
+                sums[2 * g + 1] = a;
+            }
+            group_sums(sums, tpt);
+#pragma unroll
+            for (int g = 0; g < G; ++g) {
+                const int j = j0 + g;
+                const float ss = sums[2 * g], a = sums[2 * g + 1];
                 if (tok_ok && j < k && tid == 0 && !ok[g]) d_topk_w[t * k + j] = 0.f;
                 if (!ok[g]) continue;
                 named = true;
