@@ -106,16 +106,18 @@ __device__ __forceinline__ void group_sums(float (&v)[N], int width) {
         }
 }
 
-// Rows of up to 32 vectors: tpt threads per token (a power of two), one vector
-// each, several tokens in a wave.
+constexpr int kNarrowRows = 4;   // rows of an item
+
+// Rows of up to 32 vectors: tpt threads per item of a token's rows (a power of
+// two), one vector each, several items in a wave.
 __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
     const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
     const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
     float gain_center, float eps, int T, int H, int k, int tpt, int32_t* __restrict__ owner,
     u32x4* __restrict__ d_rows, float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
-    constexpr int G = 4;   // rows in flight
+    constexpr int G = kNarrowRows;
     extern __shared__ float gain_lds[];
-    const int groups = kSmallBlock / tpt;   // tokens of a block
+    const int groups = kSmallBlock / tpt;   // items of a block
     const int sub = static_cast<int>(threadIdx.x) / tpt;
     const int tid = static_cast<int>(threadIdx.x) - sub * tpt;
     const int nvec = H >> 3;
@@ -127,75 +129,116 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
         gain[e] = mine ? gain_center + norm_w[tid * 8 + e] : 0.f;
         dgain[0][e] = 0.f;
     }
-    const long long stride = static_cast<long long>(gridDim.x) * groups;
-    for (long long t0 = static_cast<long long>(blockIdx.x) * groups; t0 < T; t0 += stride) {
-        const long long t = t0 + sub;
-        const bool tok_ok = t < T;
-        u32x4 y = {0, 0, 0, 0};
-        if (tok_ok && mine) y = d_out[t * nvec + tid];
-        float acc[8] = {};   // sum over the slots of w rstd x
-        bool named = false;
-        for (int j0 = 0; j0 < k; j0 += G) {
-            u32x4 x[G];
-            float wt[G];
-            int row[G];
-            bool ok[G];
+    // Items of G picks of a token, item u by group u mod (groups of the grid): a
+    // token's items go to neighbouring groups, whose sums for the gain meet in the
+    // block's. An item's rows are loaded while the item before it is worked on, its
+    // slots one item earlier still. ub, the block's first item, counts the turns,
+    // so that every thread takes the same ones.
+    const int per_token = (k + G - 1) / G;
+    const long long items = static_cast<long long>(T) * per_token;
+    const unsigned stride = gridDim.x * groups;
+    const int step_t = static_cast<int>(stride / per_token), step_j = static_cast<int>(stride % per_token) * G;
+    struct Place {
+        long long t;
+        int j;
+    };
+    auto advance = [&](Place& p) {
+        p.t += step_t;
+        p.j += step_j;
+        if (p.j >= per_token * G) {
+            p.j -= per_token * G;
+            ++p.t;
+        }
+    };
+    struct Item {
+        int row[G];   // -1: none, or not to be read
+        float w[G];
+    };
+    auto load_item = [&](const Place& at, Item& p) {
 #pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int j = j0 + g;
-                row[g] = -1;
-                wt[g] = 0.f;
-                if (tok_ok && j < k) {
-                    row[g] = slots[t * k + j];
-                    wt[g] = topk_w[t * k + j];
-                }
-                ok[g] = row[g] >= 0 && row[g] < R;
-                x[g] = u32x4{0, 0, 0, 0};
-                if (ok[g] && mine) x[g] = load_nt(&expert_out[static_cast<size_t>(row[g]) * nvec + tid]);
-            }
-            float sums[2 * G];
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                float ss = 0.f, a = 0.f;
-#pragma unroll
-                for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][q], ss);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) a = __builtin_fmaf(bf16_at(x[g], e), bf16_at(y, e) * gain[e], a);
-                sums[2 * g] = ss;
-                sums[2 * g + 1] = a;
-            }
-            group_sums(sums, tpt);
-#pragma unroll
-            for (int g = 0; g < G; ++g) {
-                const int j = j0 + g;
-                const float ss = sums[2 * g], a = sums[2 * g + 1];
-                if (tok_ok && j < k && tid == 0 && !ok[g]) d_topk_w[t * k + j] = 0.f;
-                if (!ok[g]) continue;
-                named = true;
-                const float rstd = 1.0f / sqrtf(ss * inv_h + eps);
-                const float ra = rstd * a;
-                if (tid == 0) {
-                    d_topk_w[t * k + j] = ra;
-                    owner[row[g]] = static_cast<int32_t>(t * k + j);
-                }
-                const float c = wt[g] * rstd;
-                const float d = rstd * (ra * inv_h);
-                float o[8];
-#pragma unroll
-                for (int e = 0; e < 8; ++e) {
-                    const float xe = bf16_at(x[g], e);
-                    acc[e] = __builtin_fmaf(c, xe, acc[e]);
-                    o[e] = c * __builtin_fmaf(-xe, d, bf16_at(y, e) * gain[e]);
-                }
-                if (mine)
-                    store_nt(u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
-                                   cvt_pk_bf16(o[6], o[7])},
-                             &d_rows[static_cast<size_t>(row[g]) * nvec + tid]);
+        for (int g = 0; g < G; ++g) {
+            p.row[g] = -1;
+            p.w[g] = 0.f;
+            if (at.t < T && at.j + g < k) {
+                p.row[g] = slots[at.t * k + at.j + g];
+                p.w[g] = topk_w[at.t * k + at.j + g];
             }
         }
-        if (named)   // the output's gradient of other tokens may hold NaN
+    };
+    auto load_rows = [&](const Place& at, Item& p, u32x4 (&x)[G], u32x4& y) {
+        y = at.t < T && mine ? d_out[at.t * nvec + tid] : u32x4{0, 0, 0, 0};
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            if (p.row[g] < 0 || p.row[g] >= R) p.row[g] = -1;
+            x[g] = u32x4{0, 0, 0, 0};
+            if (p.row[g] >= 0 && mine) x[g] = load_nt(&expert_out[static_cast<size_t>(p.row[g]) * nvec + tid]);
+        }
+    };
+    long long ub = static_cast<long long>(blockIdx.x) * groups;
+    const unsigned u = blockIdx.x * groups + sub;
+    Place at = {u / per_token, static_cast<int>(u % per_token) * G};
+    Place at1 = at;
+    advance(at1);
+    Place at2 = at1;
+    Item item, next, after;
+    u32x4 x[G], xn[G], y, yn;
+    load_item(at, item);
+    load_item(at1, next);
+    load_rows(at, item, x, y);
+    for (; ub < items; ub += stride) {
+        advance(at2);
+        load_item(at2, after);
+        load_rows(at1, next, xn, yn);
+        float sums[2 * G];
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            float ss = 0.f, a = 0.f;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) ss = dot2_sq(x[g][q], ss);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) a = __builtin_fmaf(bf16_at(x[g], e), bf16_at(y, e) * gain[e], a);
+            sums[2 * g] = ss;
+            sums[2 * g + 1] = a;
+        }
+        group_sums(sums, tpt);
+        float acc[8] = {};   // sum over the item's picks of w rstd x
+        bool named = false;
+#pragma unroll
+        for (int g = 0; g < G; ++g) {
+            const int j = at.j + g;
+            const bool ok = item.row[g] >= 0;
+            const float rstd = 1.0f / sqrtf(sums[2 * g] * inv_h + eps);
+            const float ra = ok ? rstd * sums[2 * g + 1] : 0.f;
+            if (tid == 0 && at.t < T && j < k) {
+                d_topk_w[at.t * k + j] = ra;
+                if (ok) owner[item.row[g]] = static_cast<int32_t>(at.t * k + j);
+            }
+            if (!ok) continue;
+            named = true;
+            const float c = item.w[g] * rstd;
+            const float d = rstd * (ra * inv_h);
+            float o[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float xe = bf16_at(x[g], e);
+                acc[e] = __builtin_fmaf(c, xe, acc[e]);
+                o[e] = c * __builtin_fmaf(-xe, d, bf16_at(y, e) * gain[e]);
+            }
+            if (mine)
+                store_nt(u32x4{cvt_pk_bf16(o[0], o[1]), cvt_pk_bf16(o[2], o[3]), cvt_pk_bf16(o[4], o[5]),
+                               cvt_pk_bf16(o[6], o[7])},
+                         &d_rows[static_cast<size_t>(item.row[g]) * nvec + tid]);
+        }
+        if (named)   // the output's gradient of a token without a slot may hold NaN
 #pragma unroll
             for (int e = 0; e < 8; ++e) dgain[0][e] = __builtin_fmaf(bf16_at(y, e), acc[e], dgain[0][e]);
+        at = at1;
+        at1 = at2;
+        item = next;
+        next = after;
+        y = yn;
+#pragma unroll
+        for (int g = 0; g < G; ++g) x[g] = xn[g];
     }
     if (part_gain)
         store_gain_part<1, kSmallBlock>(dgain, sub, tid, tpt, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
@@ -550,9 +593,11 @@ inline CombineBackwardPlan plan_combine_backward(int T, int R, int H) {
     }
     p.vpt = ceil_div(nvec, p.tpt);
     p.groups = p.block / p.tpt;
-    const int need = ceil_div(T, p.groups);
+    // narrow rows: T k / kNarrowRows items, of any k the workspace may be used with
+    const long long units = p.tpt < kWave ? static_cast<long long>(T) * (MOE_MAX_TOPK / kNarrowRows) : T;
+    const long long need = (units + p.groups - 1) / p.groups;
     const int most = 512;   // two blocks a CU
-    p.grid = need < most ? need : most;
+    p.grid = static_cast<int>(need < most ? need : most);
     p.owner = 0;
     p.gain = round256(sizeof(int32_t) * static_cast<size_t>(R));
     p.bytes = p.gain + round256(sizeof(float) * static_cast<size_t>(p.grid) * H);
@@ -585,8 +630,12 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
     if (!norm_w || (R > 0 && (!expert_out || !d_expert_out))) return MOE_ERR_NULL_ARG;
     if (!all_aligned16(d_out, expert_out, slots, topk_w, norm_w, d_expert_out, d_topk_w, d_norm_w))
         return MOE_ERR_ALIGN;
-    const CombineBackwardPlan p = plan_combine_backward(T, R, H);
+    CombineBackwardPlan p = plan_combine_backward(T, R, H);
     if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
+    if (p.tpt < kWave) {
+        const int need = ceil_div(static_cast<long long>(T) * ceil_div(k, kNarrowRows), p.groups);
+        if (need < p.grid) p.grid = need;
+    }
     auto* owner = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + p.owner);
     auto* part = d_norm_w ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.gain) : nullptr;
     const auto* y = reinterpret_cast<const u32x4*>(d_out);
