@@ -10,9 +10,12 @@
 //   dg_i = sum over slots of w rstd x_i y_i
 //
 // Bound by HBM: every expert row is read once and its gradient written once,
-// and y is read once per token. So one group of threads takes a token, keeps y
-// in registers for its k rows and each row in registers between the sums and
-// the gradient. Blocks are persistent over tokens, so that the gain's gradient
+// and y is read once per token. So one group of threads takes a token (a part of
+// its picks, if the tokens are few), keeps y in registers for its k rows and each
+// row in registers between the sums and the gradient. Measured: 8192 tokens of
+// 8192, k 8, 420 us and 25 us for the rows kernel (2.28 GB: 5.1 TB/s, a large
+// copy's rate); 16411 of 1032, k 22, 350 and 23 us (1.52 GB: 4.1 TB/s; rows of
+// 2064 bytes in random order begin and end within lines of 128). Blocks are persistent over tokens, so that the gain's gradient
 // is summed in registers and only one row of partial sums per block is
 // written; a last kernel adds those in block order, beside the mending below.
 //
@@ -244,18 +247,23 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_narrow_kernel(
         store_gain_part<1, kSmallBlock>(dgain, sub, tid, tpt, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
 }
 
-// A token per wave (TPT = 64) or per block (TPT = BLOCK). Thread tid of a token
-// owns vectors tid + i TPT of its rows, i < VPT. Lane j of every wave holds pick
-// j's slot and weight (k <= 32), loaded one token ahead; the rows of the next G
-// picks, the next token's first ones included, are in flight while the current
-// ones are summed and written.
+// Rows a group of the kernel below: up to 32 registers of row data, and the next
+// group's.
+constexpr int row_group(int vpt) { return vpt <= 2 ? 4 : 2; }
+
+// A token per wave (TPT = 64) or per block (TPT = BLOCK); of few tokens a part of
+// its picks, kp of them, `parts` parts a token. Thread tid of a token owns vectors
+// tid + i TPT of its rows, i < VPT. Lane j of every wave holds pick j's slot and
+// weight (k <= 32), loaded one token ahead; the rows of the next G picks, the next
+// token's first ones included, are in flight while the current ones are summed and
+// written.
 template <int VPT, int TPT, int BLOCK>
 __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void combine_backward_kernel(
     const u32x4* __restrict__ d_out, const u32x4* __restrict__ expert_out, int R,
     const int32_t* __restrict__ slots, const float* __restrict__ topk_w, const float* __restrict__ norm_w,
-    float gain_center, float eps, int T, int H, int k, int32_t* __restrict__ owner, u32x4* __restrict__ d_rows,
-    float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
-    constexpr int G = VPT <= 2 ? 4 : 2;   // rows a group: up to 32 registers of row data, and the next group's
+    float gain_center, float eps, int T, int H, int k, int parts, int kp, int32_t* __restrict__ owner,
+    u32x4* __restrict__ d_rows, float* __restrict__ d_topk_w, float* __restrict__ part_gain) {
+    constexpr int G = row_group(VPT);
     // the sum over a token's slots of w rstd x, times y once per token; with
     // four vectors a thread there are no registers for it, and each slot's
     // product goes to the gain's gradient at once
@@ -281,24 +289,31 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
             dgain[i][e] = 0.f;
         }
     }
-    auto load_picks = [&](long long t, int& r, float& w) {
+    const long long units = static_cast<long long>(T) * parts;   // < 2^31, as T k is
+    // unit u's token, and its first pick
+    auto token_of = [&](long long u) { return parts == 1 ? u : static_cast<long long>(static_cast<uint32_t>(u) / parts); };
+    auto pick_of = [&](long long u, long long t) { return parts == 1 ? 0 : static_cast<int>(u - t * parts) * kp; };
+    auto load_picks = [&](long long u, int& r, float& w) {
+        const long long t = token_of(u);
+        const int j = pick_of(u, t) + lane;
         r = -1;
         w = 0.f;
-        if (t < T && lane < k) {
-            r = slots[t * k + lane];
-            w = topk_w[t * k + lane];
+        if (u < units && lane < kp && j < k) {
+            r = slots[t * k + j];
+            w = topk_w[t * k + j];
             if (r >= R) r = -1;
         }
     };
-    auto load_token = [&](long long t, u32x4 (&y)[VPT]) {
+    auto load_token = [&](long long u, u32x4 (&y)[VPT]) {
+        const u32x4* src = d_out + token_of(u) * nvec;
 #pragma unroll
         for (int i = 0; i < VPT; ++i) {
             const int v = tid + i * TPT;
             y[i] = u32x4{0, 0, 0, 0};
-            if (t < T && v < nvec) y[i] = d_out[t * nvec + v];
+            if (u < units && v < nvec) y[i] = src[v];
         }
     };
-    // lanes k .. 63 hold slot -1, and j0 + G - 1 < 64
+    // lanes kp .. 63 hold slot -1, and j0 + G - 1 < 64
     auto load_rows = [&](int r, int j0, u32x4 (&x)[G][VPT]) {
 #pragma unroll
         for (int g = 0; g < G; ++g) {
@@ -316,27 +331,27 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
         }
     };
     const long long stride = static_cast<long long>(gridDim.x) * groups;
-    long long t = static_cast<long long>(blockIdx.x) * groups + sub;
+    long long u = static_cast<long long>(blockIdx.x) * groups + sub;
     int pick_r, next_r;
     float pick_w, next_w;
     u32x4 y[VPT], x[G][VPT];
-    load_picks(t, pick_r, pick_w);
-    load_token(t, y);
-    load_picks(t + stride, next_r, next_w);
+    load_picks(u, pick_r, pick_w);
+    load_token(u, y);
+    load_picks(u + stride, next_r, next_w);
     load_rows(pick_r, 0, x);
     int buf = 0;
     // the tokens of a block's groups start together, so that with a token per
     // block every thread takes the same turns
-    for (; t < T; t += stride) {
+    for (; u < units; u += stride) {
         float acc[SUM ? VPT : 1][8] = {};
         u32x4 yn[VPT];
         float ra_of = 0.f;   // lane j: pick j's gradient
-        for (int j0 = 0; j0 < k; j0 += G) {
+        for (int j0 = 0; j0 < kp; j0 += G) {
             u32x4 xn[G][VPT];
-            if (j0 + G < k) {
+            if (j0 + G < kp) {
                 load_rows(pick_r, j0 + G, xn);
             } else {
-                load_token(t + stride, yn);
+                load_token(u + stride, yn);
                 load_rows(next_r, 0, xn);
             }
             float sums[2 * G];
@@ -404,9 +419,11 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
 #pragma unroll
                 for (int i = 0; i < VPT; ++i) x[g][i] = xn[g][i];
         }
-        if (tid < k) {   // the token's first wave; k <= 32
-            d_topk_w[t * k + tid] = ra_of;
-            if (pick_r >= 0) owner[pick_r] = static_cast<int32_t>(t * k + tid);
+        const long long t = token_of(u);
+        const int j = pick_of(u, t) + tid;
+        if (tid < kp && j < k) {   // the token's first wave; k <= 32
+            d_topk_w[t * k + j] = ra_of;
+            if (pick_r >= 0) owner[pick_r] = static_cast<int32_t>(t * k + j);
         }
         if constexpr (SUM) {
             if (ballot(pick_r >= 0))   // the output's gradient of other tokens may hold NaN
@@ -419,7 +436,7 @@ __global__ __launch_bounds__(BLOCK) __attribute__((amdgpu_waves_per_eu(2))) void
         for (int i = 0; i < VPT; ++i) y[i] = yn[i];
         pick_r = next_r;
         pick_w = next_w;
-        load_picks(t + 2 * stride, next_r, next_w);
+        load_picks(u + 2 * stride, next_r, next_w);
     }
     if (part_gain)
         store_gain_part<VPT, BLOCK>(dgain, sub, tid, TPT, H, gain_lds, part_gain + static_cast<size_t>(blockIdx.x) * H);
@@ -569,8 +586,15 @@ __global__ __launch_bounds__(kSmallBlock) void combine_backward_rows_kernel(
     }
 }
 
+constexpr int kMostBlocks = 512;   // two a CU
+// A token's picks are shared by several units while all units fit this many blocks
+// (whole tokens / parts: 16 tokens of 2048, k 32, 41 / 12 us, 64 of 8192, k 8, 18 /
+// 15; with up to 512 blocks 256 of 8192, k 8, took 33 us in all instead of 30: each
+// block's partial sums of the gain are written and read).
+constexpr int kSplitBlocks = 256;
+
 struct CombineBackwardPlan {
-    int tpt, vpt, block, groups, grid;
+    int tpt, vpt, block, groups, rows, grid;
     size_t owner, gain, bytes;
 };
 
@@ -593,11 +617,10 @@ inline CombineBackwardPlan plan_combine_backward(int T, int R, int H) {
     }
     p.vpt = ceil_div(nvec, p.tpt);
     p.groups = p.block / p.tpt;
-    // narrow rows: T k / kNarrowRows items, of any k the workspace may be used with
-    const long long units = p.tpt < kWave ? static_cast<long long>(T) * (MOE_MAX_TOPK / kNarrowRows) : T;
-    const long long need = (units + p.groups - 1) / p.groups;
-    const int most = 512;   // two blocks a CU
-    p.grid = static_cast<int>(need < most ? need : most);
+    // at most a unit for every p.rows picks, of any k the workspace may be used with
+    p.rows = p.tpt < kWave ? kNarrowRows : row_group(p.vpt);
+    const long long need = (static_cast<long long>(T) * (MOE_MAX_TOPK / p.rows) + p.groups - 1) / p.groups;
+    p.grid = static_cast<int>(need < kMostBlocks ? need : kMostBlocks);
     p.owner = 0;
     p.gain = round256(sizeof(int32_t) * static_cast<size_t>(R));
     p.bytes = p.gain + round256(sizeof(float) * static_cast<size_t>(p.grid) * H);
@@ -632,10 +655,14 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
         return MOE_ERR_ALIGN;
     CombineBackwardPlan p = plan_combine_backward(T, R, H);
     if (!workspace || workspace_bytes < p.bytes || !aligned16(workspace)) return MOE_ERR_WORKSPACE;
-    if (p.tpt < kWave) {
-        const int need = ceil_div(static_cast<long long>(T) * ceil_div(k, kNarrowRows), p.groups);
-        if (need < p.grid) p.grid = need;
-    }
+    // narrow rows: an item for every p.rows picks; else a token's picks in more
+    // parts while those of all tokens fit a block a CU
+    int kp = p.tpt < kWave ? p.rows : k;
+    while (kp > p.rows && static_cast<long long>(T) * ceil_div(k, ceil_div(kp, 2 * p.rows) * p.rows) <= kSplitBlocks * p.groups)
+        kp = ceil_div(kp, 2 * p.rows) * p.rows;
+    const int parts = ceil_div(k, kp);
+    const int need = ceil_div(static_cast<long long>(T) * parts, p.groups);
+    if (need < p.grid) p.grid = need;
     auto* owner = reinterpret_cast<int32_t*>(static_cast<char*>(workspace) + p.owner);
     auto* part = d_norm_w ? reinterpret_cast<float*>(static_cast<char*>(workspace) + p.gain) : nullptr;
     const auto* y = reinterpret_cast<const u32x4*>(d_out);
@@ -646,7 +673,7 @@ extern "C" int moe_combine_backward(const uint16_t* d_out, const uint16_t* exper
         const size_t lds = p.groups > 1 ? sizeof(float) * static_cast<size_t>(p.groups) * H : 0;
         auto run = [&](auto kern) {
             return launch(kern, dim3(p.grid), dim3(p.block), lds, stream, y, x, R, slots, topk_w, norm_w, gain_center,
-                          eps, T, H, k, owner, dx, d_topk_w, part);
+                          eps, T, H, k, parts, kp, owner, dx, d_topk_w, part);
         };
         if (p.tpt < kWave)
             st = launch(combine_backward_narrow_kernel, dim3(p.grid), dim3(p.block), lds, stream, y, x, R, slots,

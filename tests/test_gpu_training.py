@@ -522,7 +522,8 @@ def test_combine_backward_widths(H):
 
 @pytest.mark.parametrize("T,H,k", [(1, 64, 1), (1, 8192, 8), (2, 1024, 32), (16, 256, 4), (700, 1024, 22),
                                    (1500, 16, 3), (600, 2304, 2), (530, 4096, 9), (1100, 4104, 3),
-                                   (5000, 520, 2), (70000, 16, 2), (600, 16384, 1)])
+                                   (5000, 520, 2), (70000, 16, 2), (600, 16384, 1), (1, 16, 32), (5, 56, 25),
+                                   (3, 1032, 31), (100, 520, 13), (90, 4104, 9), (20, 8200, 7), (255, 2048, 6)])
 def test_combine_backward_tokens(T, H, k):
     _check_combine(np.random.default_rng(T + H), T, H, k)
 
