@@ -19,6 +19,13 @@
 // results do not depend on timing. A batch of up to kSmallTokens tokens takes
 // one block of sixteen waves instead, which needs no second kernel and no
 // workspace: at such sizes a launch costs more than the work.
+//
+// Measured (forward, its addition, backward): 8111 tokens of 254 experts in 13
+// sequences 8.7, 7.2 and 9.1 us, a chain of dependent steps each (16 MB are 3 us at
+// a copy's 5.1 TB/s); 32768 of 512 14.9 (4.5 TB/s), 8.7 and 23.8 us (5.6 TB/s);
+// 16 tokens of 16 4.6 and 3.7 us. Distillation: 4093 tokens of 2560 11.2 (3.8
+// TB/s), 3.4 and 18.2 us (4.6 TB/s); 8192 of 256 9.1, 2.9 and 8.8 us; one token of
+// 64 3.1 and 2.7 us.
 #include "launch.hpp"
 #include "scores.hpp"
 
@@ -27,14 +34,30 @@ namespace {
 
 constexpr int kMaxChunk = 64;         // tokens of a block: one ballot holds their validity
 constexpr int kGroups = 4;            // tokens of a block at a time where a wave takes a row
-constexpr int kTargetBlocks = 1024;   // four such blocks a CU
-constexpr int kFewTokens = 512;       // up to these a block takes one token of the balance loss: with many short
-                                      // sequences (15 tokens in 42) four tokens' sequences in turn took 18 us
+// Four such blocks a CU: with 512 / 1024 / 2048 of them, 32768 tokens of 512 experts
+// took 15.9, 14.7 and 16.0 us, their parts' addition 9.4, 11.2 and 15.8, the
+// gradient 24.5, 23.7 and 23.8.
+constexpr int kTargetBlocks = 1024;
+// Up to these a block takes one token of the balance loss: 500 tokens in 60
+// sequences 4.3 us, by four tokens, with their sequences in turn, 6.5; in one
+// sequence 4.3 and 4.2.
+constexpr int kFewTokens = 512;
+// By one block, if their rows take one wave, with up to kSmallSequences sequences in
+// turn: one launch saves 3.5 us of an eager call, and its kernel takes no longer
+// than the two others up to here (balance, 32 tokens of 64 experts 6.1 us against
+// 4.1 + 5.5, of 1024 10.3 against 5.7 + 6.1, of 256 in four sequences 10.7 against
+// 4.2 + 5.9; distillation of 16 4.9 against 4.1 + 2.1, of 32 8.2 against 4.4 + 1.8);
+// 64 tokens of 1024 took 16.8 against 12.3, their distillation 21.2 against 6.9.
 constexpr int kSmallGroups = 16;
-constexpr int kSmallTokens = 64;      // by one block, if their rows take one wave
+constexpr int kSmallTokens = 32;
 constexpr int kSmallExperts = 1024;
-constexpr int kBalanceOneWave = 1024, kDistillOneWave = 2560;   // widest rows that one wave takes
-constexpr int kSmallSequences = 4;    // taken in turn there
+constexpr int kSmallSequences = 4;
+// Widest rows that one wave takes; several waves need fewer registers each, but a
+// barrier a sum. Balance, forward and gradient, one wave / several: 4096 tokens of
+// 1500 experts 13.6 + 22.1 / 15.9 + 19.6 us, of 2560 21.2 + 46.3 / 19.9 + 27.9.
+// Distillation keeps fewer arrays: of 1500 11.2 + 12.9 / 18.8 + 19.2, of 2560 15.3 +
+// 20.8 / 25.4 + 27.3.
+constexpr int kBalanceOneWave = 1024, kDistillOneWave = 2560;
 
 inline bool small_batch(int T, int E) { return T <= kSmallTokens && E <= kSmallExperts; }
 

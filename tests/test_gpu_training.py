@@ -123,7 +123,7 @@ def _check_balance(g, T, E, k, S, score, spread=1.0, shift=0.0, d_losses=(0.5, 0
                                      (200, 257, 3, 66), (333, 1001, 8, 5), (130, 2560, 8, 2), (70, 4096, 32, None),
                                      (67, 4095, 2, 3), (2000, 256, 8, 130), (4500, 33, 4, 3), (50, 1500, 5, 2),
                                      (50, 2000, 5, 2), (50, 700, 5, 2), (40, 1024, 8, 3), (64, 1023, 8, 60),
-                                     (66000, 9, 2, 4)])
+                                     (66000, 9, 2, 4), (32, 1024, 8, 4), (29, 600, 5, 2), (33, 1024, 8, 4)])
 def test_balance(T, E, k, S, score):
     _check_balance(np.random.default_rng(T * 7 + E), T, E, k, S, score)
 
@@ -305,7 +305,7 @@ def _check_distill(g, T, E, K, score, temperature, edit=None, spread=1.0, shift=
                                                (300, 254, 8, 1.0), (131, 1001, 31, 4.0), (70, 2560, 8, 2.0),
                                                (41, 4096, 32, 1.0), (33, 4093, 5, 0.7), (4200, 40, 3, 1.0),
                                                (9, 5, 12, 1.0), (50, 1500, 5, 2.0), (50, 2000, 5, 1.0),
-                                               (50, 700, 5, 2.0), (50, 400, 5, 2.0), (132000, 6, 3, 1.0)])
+                                               (50, 700, 5, 2.0), (50, 400, 5, 2.0), (132000, 6, 3, 1.0), (32, 1000, 8, 1.0), (33, 900, 4, 1.0)])
 def test_distill(T, E, K, temperature, score):
     _check_distill(np.random.default_rng(T + E + K), T, E, K, score, temperature)
 
