@@ -210,7 +210,7 @@ __device__ __forceinline__ void balance_part(const Place<WPT, GROUPS>& at, const
             total[1] = u.sum();
         }
         reduce.sum(total);
-        const float lse = total[0] == 0.f ? 0.f : m + logf(total[0]);   // a row of -inf adds nothing
+        const float lse = total[0] == 0.f ? 0.f : m + log_fast(total[0]);   // a row of -inf adds nothing
         z += lse * lse;
         const float inv = inverse(total[SIGMOID ? 1 : 0]);
 #pragma unroll
@@ -535,7 +535,7 @@ __global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void balance_bac
             float v[3] = {d.sum(), u.sum(), u.dot(cf)};
             reduce.sum(v);
             // the z loss' part: (2 / n) lse softmax
-            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + logf(v[0])) * inverse(v[0]);
+            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + log_fast(v[0])) * inverse(v[0]);
             const float inv = inverse(v[1]), dot = v[2] * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
@@ -546,7 +546,7 @@ __global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void balance_bac
             float v[2] = {u.sum(), u.dot(cf)};
             reduce.sum(v);
             const float inv = inverse(v[0]), dot = v[1] * inv;
-            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + logf(v[0])) * inv;
+            const float zc = zg == 0.f || v[0] == 0.f ? 0.f : zg * (m + log_fast(v[0])) * inv;
 #pragma unroll
             for (int i = 0; i < NV; ++i)
 #pragma unroll
@@ -628,9 +628,9 @@ __device__ __forceinline__ bool teacher_shares(const Entry& e, int E, int score,
     if (ballot(id >= 0) == 0) return false;
     const float z = id < 0 ? kNegInf : log_score(e.z * inv_temp, score);
     const float m = wave_max(z);
-    const float w = id < 0 ? 0.f : expf(z - m);
+    const float w = id < 0 ? 0.f : exp_fast(z - m);
     const float total = wave_sum(w);
-    logq = id < 0 ? 0.f : (z - m) - logf(total);
+    logq = id < 0 ? 0.f : (z - m) - log_fast(total);
     q = w / total;
     return true;
 }
@@ -662,14 +662,18 @@ __global__ __launch_bounds__(WPT* GROUPS* kWave) void distill_kernel(
     const bool writes = at.lane == 0 && at.part == 0;
     float sum = 0.f;
     int32_t n = 0;
+    int have = at.group;   // the token that entry belongs to
     for_rows(valid & share, rows, E, at.part, at.lane, first, at.group, [&](int t, Row<NV, WPT>& x) {
         const size_t tok = static_cast<size_t>(t0) + t;
-        if (t != at.group) entry = teacher_entry(t_ids, t_logits, tok, K);
+        if (t != have) entry = teacher_entry(t_ids, t_logits, tok, K);
         float xp = 0.f;   // the student's logit of the entry
         if (entry.id >= 0 && entry.id < E) xp = logits[tok * E + entry.id] * inv_temp;
+        const Entry mine = entry;
+        have = t + GROUPS;   // the group's next token, likely valid
+        if (have < len) entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + have, K);
         int id = -1;
         float q = 0.f, logq = 0.f, loss = 0.f;
-        if (teacher_shares(entry, E, score, inv_temp, id, q, logq)) {
+        if (teacher_shares(mine, E, score, inv_temp, id, q, logq)) {
             Row<NV, WPT> u;
             x.scale(inv_temp);
             float m = weight_origin(reduce.max(x.max()));
@@ -683,7 +687,7 @@ __global__ __launch_bounds__(WPT* GROUPS* kWave) void distill_kernel(
             reduce.sum(total);
             // an expert that the student masks is infinitely far, in a row of -inf too
             const float ls = log_score(xp, score);
-            const float logp = ls == kNegInf ? kNegInf : ls - (m + logf(total[0]));
+            const float logp = ls == kNegInf ? kNegInf : ls - (m + log_fast(total[0]));
             const float term = id >= 0 && q > 0.f ? q * (logq - logp) : 0.f;
             loss = temp2 * wave_sum(term);
             sum += loss;
@@ -762,11 +766,15 @@ __global__ __launch_bounds__((WPT > 1 ? WPT : kGroups) * kWave) void distill_bac
     const uint64_t valid = valid_tokens(mask, t0, len);
     const uint64_t share = at.share() & bit_range(0, len);
     const float g = d_loss[0] * temp / static_cast<float>(max(tokens[0], 1));
+    int have = at.group;   // the token that entry belongs to
     for_rows(valid & share, rows, E, at.part, at.lane, first, at.group, [&](int t, Row<NV, WPT>& x) {
-        if (t != at.group) entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + t, K);
+        if (t != have) entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + t, K);
+        const Entry now = entry;
+        have = t + (WPT > 1 ? 1 : kGroups);   // the group's next token, likely valid
+        if (have < len) entry = teacher_entry(t_ids, t_logits, static_cast<size_t>(t0) + have, K);
         int id = -1;
         float q = 0.f, logq = 0.f;
-        if (!teacher_shares(entry, E, score, inv_temp, id, q, logq)) {
+        if (!teacher_shares(now, E, score, inv_temp, id, q, logq)) {
             x.fill(0.f);
             if (!accumulate) x.store(out + static_cast<size_t>(t) * E, E, at.part, at.lane, false);
             return;

@@ -29,6 +29,10 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // near one ulp where the result counts.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
+// log(x) of a sum of weights, which is at least 1/2 or 0: within an ulp of it and
+// 2^-24 near 1, as the exponentials it comes from.
+__device__ __forceinline__ float log_fast(float x) { return __builtin_amdgcn_logf(x) * 0.693147180559945309417f; }
+
 // Maximum over the wave (same exchanges as wave_sum). NaN is ignored unless
 // every lane holds one.
 __device__ __forceinline__ float wave_max(float v) {
@@ -224,7 +228,7 @@ __device__ __forceinline__ void sigmoid_weights(const Row<NV, WPT>& x, float m, 
 // log of the score of one logit (the sigmoid's, or the logit itself).
 __device__ __forceinline__ float log_score(float x, int score) {
     if (score == MOE_SCORE_SOFTMAX) return x;
-    return fminf(x, 0.f) - log1pf(expf(-fabsf(x)));
+    return fminf(x, 0.f) - log_fast(1.f + exp_fast(-fabsf(x)));
 }
 
 // ---- sequences of tokens ----------------------------------------------------
