@@ -21,11 +21,12 @@
 // workspace: at such sizes a launch costs more than the work.
 //
 // Measured (forward, its addition, backward): 8111 tokens of 254 experts in 13
-// sequences 8.7, 7.2 and 9.1 us, a chain of dependent steps each (16 MB are 3 us at
-// a copy's 5.1 TB/s); 32768 of 512 14.9 (4.5 TB/s), 8.7 and 23.8 us (5.6 TB/s);
-// 16 tokens of 16 4.6 and 3.7 us. Distillation: 4093 tokens of 2560 11.2 (3.8
-// TB/s), 3.4 and 18.2 us (4.6 TB/s); 8192 of 256 9.1, 2.9 and 8.8 us; one token of
-// 64 3.1 and 2.7 us.
+// sequences 8.3, 7.2 and 8.8 us, a chain of dependent steps each (16 MB are 3 us at
+// a copy's 5.1 TB/s); 32768 of 512 14.7 (4.6 TB/s), 8.8 and 23.5 us (5.7 TB/s);
+// 16 tokens of 16 4.3 and 3.7 us. Distillation: 4093 tokens of 2560 11.1 (3.8
+// TB/s), 3.1 and 16.5 us (5.1 TB/s); 8192 of 256 5.8, 2.2 and 7.5 us; one token of
+// 64 2.5 and 2.4 us. The choices below were measured before the sigmoid and the
+// logarithms took their present forms, which shortens both sides alike.
 #include "launch.hpp"
 #include "scores.hpp"
 
@@ -630,7 +631,7 @@ __device__ __forceinline__ bool teacher_shares(const Entry& e, int E, int score,
     const float m = wave_max(z);
     const float w = id < 0 ? 0.f : exp_fast(z - m);
     const float total = wave_sum(w);
-    logq = id < 0 ? 0.f : (z - m) - log_fast(total);
+    logq = id < 0 ? 0.f : (z - m) - logf(total);
     q = w / total;
     return true;
 }
@@ -687,7 +688,7 @@ __global__ __launch_bounds__(WPT* GROUPS* kWave) void distill_kernel(
             reduce.sum(total);
             // an expert that the student masks is infinitely far, in a row of -inf too
             const float ls = log_score(xp, score);
-            const float logp = ls == kNegInf ? kNegInf : ls - (m + log_fast(total[0]));
+            const float logp = ls == kNegInf ? kNegInf : (ls - m) - logf(total[0]);
             const float term = id >= 0 && q > 0.f ? q * (logq - logp) : 0.f;
             loss = temp2 * wave_sum(term);
             sum += loss;

@@ -29,8 +29,7 @@ constexpr float kNegInf = -__builtin_huge_valf();
 // near one ulp where the result counts.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2e); }
 
-// log(x) of a sum of weights, which is at least 1/2 or 0: within an ulp of it and
-// 2^-24 near 1, as the exponentials it comes from.
+// log(x) for x >= 1/2 or 0, by the hardware's base 2 logarithm.
 __device__ __forceinline__ float log_fast(float x) { return __builtin_amdgcn_logf(x) * 0.693147180559945309417f; }
 
 // Maximum over the wave (same exchanges as wave_sum). NaN is ignored unless
@@ -228,7 +227,9 @@ __device__ __forceinline__ void sigmoid_weights(const Row<NV, WPT>& x, float m, 
 // log of the score of one logit (the sigmoid's, or the logit itself).
 __device__ __forceinline__ float log_score(float x, int score) {
     if (score == MOE_SCORE_SOFTMAX) return x;
-    return fminf(x, 0.f) - log_fast(1.f + exp_fast(-fabsf(x)));
+    // log(1 + e) with what 1 + e rounds off
+    const float e = exp_fast(-fabsf(x)), y = 1.f + e;
+    return fminf(x, 0.f) - __builtin_fmaf(e - (y - 1.f), __builtin_amdgcn_rcpf(y), log_fast(y));
 }
 
 // ---- sequences of tokens ----------------------------------------------------
